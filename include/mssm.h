@@ -442,6 +442,190 @@ int mssm_selective_scan_fwd_plan(const mssm_dims* dims, mssm_plan* plan);
 int mssm_set_scan_timing_events(void* start, void* stop);
 
 /*
+ * ---- The layer around the scans.
+ *
+ * The norm that joins the residual stream, the 8-bit products of the block's
+ * projections, the Mamba-2 single-token step with its convolution, and the
+ * choice of the next token.  Memory, streams and errors are as above; these
+ * calls allocate nothing, and those that need a workspace take it from the
+ * caller (256-byte aligned, of the size that the call's _workspace function
+ * gives for the device that is current).
+ *
+ * 8-bit values are e4m3 (1 sign, 4 exponent and 3 mantissa bits, largest value
+ * 448, no infinity).  Each block of 128 of them has a scale that is a power of
+ * two, held as its biased exponent in one byte (e8m0: 2^(byte - 127)); a
+ * value stands for e4m3 * scale.  A quantised block takes the smallest scale
+ * s with max |block| / s <= 448, an all-zero one 2^-127.  An infinity or NaN
+ * becomes NaN and leaves its block's scale alone.
+ */
+typedef struct {
+  int64_t rows;      /* >= 1                                               */
+  int64_t dim;       /* columns, 1 to 32768                                */
+  int64_t x_stride;  /* elements from one row of x to the next; 0 = dim    */
+  int32_t io_dtype;  /* mssm_dtype of x and out (dout and dx)              */
+  int32_t res_dtype; /* mssm_dtype of the residual stream                  */
+  float eps;         /* >= 0                                               */
+  int32_t reserved;
+} mssm_norm_dims;
+
+/*
+ * Root-mean-square norm with the residual's addition, per row in fp32:
+ *     r = x + residual;  rstd = 1 / sqrt(mean(r^2) + eps);
+ *     out = r * rstd * weight
+ *   x            : (rows, dim) io dtype, rows x_stride apart
+ *   residual     : (rows, dim) residual dtype, or NULL (r = x)
+ *   weight       : (dim) fp32
+ *   out          : (rows, dim) io dtype
+ *   residual_out : (rows, dim) residual dtype receiving r, or NULL; it may be
+ *                  `residual` itself (updated in place)
+ *   rstd         : (rows) fp32, or NULL
+ * The norm is of the unrounded r.
+ */
+int mssm_rms_norm_fwd(const void* x, const void* residual, const float* weight, void* out,
+                      void* residual_out, float* rstd, const mssm_norm_dims* dims, void* stream);
+
+/* The same with the output in 8 bits: q (rows, dim) e4m3, scales
+ * (rows, ceil(dim / 128)) e8m0. */
+int mssm_rms_norm_fwd_fp8(const void* x, const void* residual, const float* weight, void* q,
+                          void* scales, void* residual_out, float* rstd,
+                          const mssm_norm_dims* dims, void* stream);
+
+/*
+ * Gradients of the norm, with xhat = r * rstd:
+ *     dr      = rstd * (weight dout - xhat mean(weight dout xhat)) + dresidual
+ *     dweight = sum over rows of dout xhat
+ *   dout      : (rows, dim) io dtype
+ *   r, rstd   : the forward call's residual_out (x where it had no residual;
+ *               io dtype then) and rstd
+ *   dresidual : (rows, dim) residual dtype, the gradient of residual_out from
+ *               its later uses, or NULL
+ *   dx        : (rows, dim) io dtype receiving dr
+ *   dr        : (rows, dim) residual dtype receiving dr, or NULL
+ *   dweight   : (dim) fp32
+ * has_residual: nonzero when the forward call had a residual; dresidual and dr
+ * must be NULL otherwise.  The rows are contiguous (x_stride 0 or dim).  The
+ * sums over rows are taken in a fixed order: equal calls give equal bits.
+ */
+int mssm_rms_norm_bwd(const void* dout, const void* r, const float* weight, const float* rstd,
+                      const void* dresidual, void* dx, void* dr, float* dweight, void* workspace,
+                      int64_t workspace_bytes, const mssm_norm_dims* dims, int has_residual,
+                      void* stream);
+int mssm_rms_norm_bwd_workspace(const mssm_norm_dims* dims, int64_t* bytes);
+
+typedef struct {
+  int64_t rows, cols;  /* of x, >= 1                                        */
+  int64_t x_stride;    /* elements from one row of x to the next; 0 = cols  */
+  int32_t io_dtype;    /* mssm_dtype of x                                   */
+  int32_t block_rows;  /* 1: a scale for each 128 along a row of q;         */
+                       /* 128: one for each 128 x 128 block                 */
+  int32_t transpose;   /* nonzero: q is x transposed, (cols, rows)          */
+  int32_t reserved;
+} mssm_quant_dims;
+
+/*
+ * x in 8 bits: q (rows, cols) e4m3, or (cols, rows) with transpose, and its
+ * scales (ceil(q's rows / block_rows), ceil(q's columns / 128)) e8m0.
+ */
+int mssm_quantize_fp8(const void* x, void* q, void* scales, const mssm_quant_dims* dims,
+                      void* stream);
+
+typedef struct {
+  int64_t m, n, k;       /* >= 1; k at most 2^22                            */
+  int32_t out_dtype;     /* mssm_dtype of out                               */
+  int32_t b_block_rows;  /* rows of b that share a scale: 1 or 128          */
+} mssm_matmul_dims;
+
+/*
+ * out = a b^T over 8-bit values with a scale for each block of 128 along k:
+ *   a : (m, k) e4m3, a_scales (m, ceil(k / 128)) e8m0
+ *   b : (n, k) e4m3, b_scales (ceil(n / b_block_rows), ceil(k / 128)) e8m0
+ *   out : (m, n) out dtype, summed in fp32 and rounded once
+ * A linear layer's three products: out = x w^T with b = w (128 x 128 blocks);
+ * dx = dout w with a = dout in row blocks and b = w transposed; dw = dout^T x
+ * with both quantised transposed and b_block_rows = 1.
+ */
+int mssm_fp8_matmul(const void* a, const void* a_scales, const void* b, const void* b_scales,
+                    void* out, const mssm_matmul_dims* dims, void* stream);
+
+typedef struct {
+  int64_t rows;           /* >= 1                                           */
+  int64_t vocab;          /* tokens of a row, 1 to 2^22                     */
+  int64_t logits_stride;  /* elements from one row to the next; 0 = vocab   */
+  int64_t noise_stride;
+  int32_t io_dtype;       /* mssm_dtype of the logits                       */
+  int32_t top_k;          /* <= 0: all                                      */
+  float temperature;      /* <= 0: the likeliest token                      */
+  float top_p;            /* >= 1: all                                      */
+  float min_p;            /* <= 0: all                                      */
+  int32_t reserved;
+  /* settings of each row, (rows), in place of the values above; each may be
+   * NULL */
+  const float* temperature_row;
+  const int32_t* top_k_row;
+  const float* top_p_row;
+  const float* min_p_row;
+} mssm_sample_args;
+
+/*
+ * The next token of each row from given random numbers.  With m the row's
+ * largest logit l, w = exp((l - m) / temperature), and the tokens in order of
+ * falling logit (equal ones by rising index):
+ *   top_k keeps the first top_k; top_p keeps a token while the w before it sum
+ *   to less than top_p times the sum of the first top_k; min_p keeps
+ *   w >= min_p; the first token always stays.
+ * Of the kept tokens the one with the largest w / -log(noise) is taken (the
+ * lowest index of equal ones).
+ *   logits   : (rows, vocab) io dtype; -infinity and NaN are never taken
+ *   noise    : (rows, vocab) fp32, uniform on (0, 1)
+ *   tokens   : (rows) int64; -1 where a row has nothing to take
+ *   logprobs : (rows) fp32, the token's log-probability among the kept ones
+ *              (-infinity for token -1, 0 for the likeliest token's choice)
+ */
+int mssm_sample(const void* logits, const float* noise, int64_t* tokens, float* logprobs,
+                const mssm_sample_args* args, void* stream);
+
+typedef struct {
+  int64_t batch;      /* sequences, >= 1                                    */
+  int64_t cache;      /* rows of state and conv_state (= batch without slots) */
+  int64_t nheads;     /* a multiple of ngroups                              */
+  int64_t headdim;    /* 64                                                 */
+  int64_t ngroups;    /* B/C groups, >= 1                                   */
+  int64_t dstate;     /* 64 or 128                                          */
+  int64_t xbc_stride; /* elements from one sequence to the next in xbc, dt  */
+  int64_t dt_stride;  /* and z (rows of one projection's output, say);      */
+  int64_t z_stride;   /* 0 = contiguous                                     */
+  int32_t width;      /* of the convolution, 2 to 4                         */
+  int32_t io_dtype;   /* mssm_dtype of xbc, dt, z, conv_state, out          */
+} mssm_step_dims;
+
+/*
+ * Single-token step of the Mamba-2 block: mssm_causal_conv1d_fwd (with silu)
+ * over the x, B and C channels and mssm_mamba2_scan_fwd, for one token of each
+ * sequence, both states updated in place.  channels = nheads * headdim
+ * + 2 * ngroups * dstate, the x channels first, then B, then C.
+ *   state      : (cache, nheads * headdim, dstate) fp32, as the scan's
+ *                last_state
+ *   conv_state : (cache, channels, width - 1) io dtype, the inputs before this
+ *                one, as the convolution's init
+ *   xbc        : (batch, channels);  dt : (batch, nheads) raw steps
+ *   z          : (batch, nheads * headdim) gate, or NULL
+ *   conv_weight: (channels, width) fp32;  conv_bias : (channels) fp32 or NULL
+ *   A, D, dt_bias : (nheads) fp32; D and dt_bias may be NULL (zero)
+ *   slots      : (batch) int32, the row of the states that belongs to each
+ *                sequence, or NULL (row b; cache = batch then).  A value
+ *                outside [0, cache) marks padding: its out is zero and no
+ *                state is touched.  No two sequences may share a row.
+ *   out        : (batch, nheads * headdim) io dtype
+ * The convolution's output stays in fp32.
+ */
+int mssm_mamba2_state_update(float* state, void* conv_state, const void* xbc, const void* dt,
+                             const float* conv_weight, const float* conv_bias, const float* A,
+                             const float* D, const void* z, const float* dt_bias, int softplus,
+                             const int32_t* slots, void* out, void* workspace,
+                             int64_t workspace_bytes, const mssm_step_dims* dims, void* stream);
+int mssm_mamba2_state_update_workspace(const mssm_step_dims* dims, int64_t* bytes);
+
+/*
  * Issue-rate probe of the vector ALU, for the roofline of the scan, which is
  * bound by its exponentials and fp32 multiply-adds rather than by HBM
  * (page "What are State Space Models (SSMs)?", Key Features: the selective

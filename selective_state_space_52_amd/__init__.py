@@ -23,7 +23,11 @@ from ._lib import (MSSM_BF16, MSSM_F32, MSSM_FLAG_BC_STATE_MAJOR, MSSM_FLAG_LAYO
                    MSSM_OP_MAMBA2_FWD, MSSM_OP_SCAN_BWD, MSSM_OP_SCAN_FWD,
                    MSSM_OP_SCAN_FWD_CONV, Dims, MssmError, Plan, check, lib)
 
-__all__ = ["selective_scan_fwd", "selective_scan_bwd", "selective_scan_fwd_conv",
+from .layer import (fp8_matmul, mamba2_state_update, quantize_fp8, rms_norm_bwd, rms_norm_fwd,
+                    rms_norm_fwd_fp8, sample_tokens)
+
+__all__ = ["rms_norm_fwd", "rms_norm_fwd_fp8", "rms_norm_bwd", "quantize_fp8", "fp8_matmul",
+           "sample_tokens", "mamba2_state_update", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_fwd_conv",
            "causal_conv1d_fwd", "selective_state_update", "mamba2_scan_fwd", "scan_plan",
            "workspace_size", "set_scan_timing_events", "MssmError", "abi_version"]
 

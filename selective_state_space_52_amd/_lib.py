@@ -34,7 +34,11 @@ EXPORTS = ("mssm_selective_scan_fwd", "mssm_selective_scan_bwd",
            "mssm_selective_scan_fwd_ws", "mssm_selective_scan_fwd_conv_ws",
            "mssm_selective_scan_bwd_ws", "mssm_mamba2_scan_fwd_ws",
            "mssm_workspace_size", "mssm_selective_scan_fwd_noalloc",
-           "mssm_valu_probe", "mssm_causal_conv1d_bwd")
+           "mssm_valu_probe", "mssm_causal_conv1d_bwd",
+           "mssm_rms_norm_fwd", "mssm_rms_norm_fwd_fp8", "mssm_rms_norm_bwd",
+           "mssm_rms_norm_bwd_workspace", "mssm_quantize_fp8", "mssm_fp8_matmul",
+           "mssm_sample", "mssm_mamba2_state_update",
+           "mssm_mamba2_state_update_workspace")
 
 
 class Dims(ctypes.Structure):
@@ -54,6 +58,44 @@ class Plan(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "reserved"}
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class QuantDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("transpose", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class MatmulDims(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("out_dtype", ctypes.c_int32), ("b_block_rows", ctypes.c_int32)]
+
+
+class SampleArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("logits_stride", ctypes.c_int64), ("noise_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("temperature_row", ctypes.c_void_p), ("top_k_row", ctypes.c_void_p),
+                ("top_p_row", ctypes.c_void_p), ("min_p_row", ctypes.c_void_p)]
+
+
+class StepDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("cache", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("xbc_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("z_stride", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -130,6 +172,20 @@ def lib():
         L.mssm_causal_conv1d_bwd.restype = i
         L.mssm_valu_probe.argtypes = [i, i, i, vp, vp]
         L.mssm_valu_probe.restype = i
+        def sig(name, args):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, i
+        nd, out64 = ctypes.POINTER(NormDims), ctypes.POINTER(i64)
+        sd = ctypes.POINTER(StepDims)
+        sig("mssm_rms_norm_fwd", [vp] * 6 + [nd, vp])
+        sig("mssm_rms_norm_fwd_fp8", [vp] * 7 + [nd, vp])
+        sig("mssm_rms_norm_bwd", [vp] * 9 + [i64, nd, i, vp])
+        sig("mssm_rms_norm_bwd_workspace", [nd, out64])
+        sig("mssm_quantize_fp8", [vp] * 3 + [ctypes.POINTER(QuantDims), vp])
+        sig("mssm_fp8_matmul", [vp] * 5 + [ctypes.POINTER(MatmulDims), vp])
+        sig("mssm_sample", [vp] * 4 + [ctypes.POINTER(SampleArgs), vp])
+        sig("mssm_mamba2_state_update", [vp] * 10 + [i] + [vp] * 3 + [i64, sd, vp])
+        sig("mssm_mamba2_state_update_workspace", [sd, out64])
         _lib = L
     return _lib
 

@@ -1,0 +1,149 @@
+// fp8.h -- e4m3 values with power-of-two block scales (e8m0), and 8-element
+// accesses of rows that need not be aligned.
+#pragma once
+
+#include "dev_math.h"
+
+namespace mssm {
+
+// Columns that share one scale.
+constexpr int kScaleBlock = 128;
+
+// Biased exponent of the smallest power of two s with amax / s <= 448, the
+// largest finite e4m3 value.  448 is 1.75 * 2^8, so with amax = m * 2^e and m
+// in [1, 2) s is 2^(e-8) up to m = 1.75 and 2^(e-7) above it: adding the
+// mantissa's distance from 0.75 to 1 (less one unit) carries into the
+// exponent exactly there.  An all-zero block gets the smallest scale.  A
+// power of two divides the values without rounding them, and the matrix
+// instructions take such scales themselves.
+__device__ __forceinline__ uint32_t scale_code(float amax) {
+  const int32_t c = (int32_t)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
+  return (uint32_t)max(c, 0);
+}
+// 1 / s.  amax is finite, so the code is at most 247 and the power normal.
+__device__ __forceinline__ float scale_inverse(uint32_t code) {
+  return __uint_as_float((254u - code) << 23);
+}
+
+// An infinity has no e4m3 value; it becomes NaN here, so that it neither
+// decides a block's scale (fmaxf passes NaN over) nor saturates.
+__device__ __forceinline__ float finite_or_nan(float v) {
+  return fabsf(v) <= 3.402823466e38f ? v : __builtin_nanf("");
+}
+
+// Four values within +-448 (or NaN) to e4m3, round to nearest even.
+__device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return (uint32_t)w;
+}
+
+// Wide accesses at any element's alignment: the type's alignment of 1 lets
+// the compiler use one global access of its full width, which gfx950 takes at
+// every byte address.
+struct __attribute__((packed, aligned(1))) Any8 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(1))) Any16 { uint32_t w[4]; };
+
+// v[0..7] = p[i..i+7], the values past `n` of them zero.
+template <bool BF16>
+__device__ __forceinline__ void load8(float (&v)[8], const void* p, int64_t i, int n) {
+  if constexpr (BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if (n >= 8) {
+      const Any16 a = *reinterpret_cast<const Any16*>(q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(a.w[j]);
+        v[2 * j + 1] = bf16_hi(a.w[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? bf16_bits(q[j]) : 0.0f;
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + i;
+    if (n >= 8) {
+      const Any16 a = reinterpret_cast<const Any16*>(q)[0];
+      const Any16 b = reinterpret_cast<const Any16*>(q)[1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = __uint_as_float(a.w[j]);
+        v[4 + j] = __uint_as_float(b.w[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint16_t* q = static_cast<uint16_t*>(p) + i;
+    if (n >= 8) {
+      Any16 a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a.w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<Any16*>(q) = a;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[j] = to_bf16(v[j]);
+    }
+  } else {
+    float* q = static_cast<float*>(p) + i;
+    if (n >= 8) {
+      Any16 a, b;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a.w[j] = __float_as_uint(v[j]);
+        b.w[j] = __float_as_uint(v[4 + j]);
+      }
+      reinterpret_cast<Any16*>(q)[0] = a;
+      reinterpret_cast<Any16*>(q)[1] = b;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) q[j] = v[j];
+    }
+  }
+}
+
+__device__ __forceinline__ void store8_fp8(uint8_t* p, int n, uint32_t lo, uint32_t hi) {
+  if (n >= 8) {
+    *reinterpret_cast<Any8*>(p) = Any8{{lo, hi}};
+  } else {
+    const uint64_t w = (uint64_t)hi << 32 | lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = (uint8_t)(w >> (8 * j));
+  }
+}
+
+// Largest / sum over aligned groups of 16 lanes (DPP moves inside a row of 16
+// lanes: a quad's lanes, then the mirrored lane of each 8 and of each 16),
+// every lane getting the result; fmaxf passes a NaN over.
+template <int CTRL>
+__device__ __forceinline__ float dpp_row(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp_row<0xB1>(v));
+  v = fmaxf(v, dpp_row<0x4E>(v));
+  v = fmaxf(v, dpp_row<0x141>(v));
+  return fmaxf(v, dpp_row<0x140>(v));
+}
+__device__ __forceinline__ float sum16(float v) {
+  v += dpp_row<0xB1>(v);
+  v += dpp_row<0x4E>(v);
+  v += dpp_row<0x141>(v);
+  return v + dpp_row<0x140>(v);
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+}  // namespace mssm

@@ -199,6 +199,21 @@ int make_plan(const mssm_dims* dims, int cus, mssm_plan* plan) {
 
 }  // namespace
 
+namespace mssm {
+
+void set_hip_error(const char* what, hipError_t e) { ::set_hip_error(what, e); }
+
+int check_workspace(const void* ws, int64_t ws_bytes, int64_t need) {
+  return ::check_workspace(ws, ws_bytes, need);
+}
+
+int compute_units() {
+  refresh_cu_count();
+  return g_cu_count > 0 ? g_cu_count : kDefaultCUs;
+}
+
+}  // namespace mssm
+
 extern "C" {
 
 int mssm_abi_version(void) { return MSSM_ABI_VERSION; }

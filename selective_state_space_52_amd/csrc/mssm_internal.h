@@ -273,4 +273,107 @@ void mamba2_plan(int64_t pairs, int64_t L, int cus, int forced, Mamba2Params* p)
 int64_t mamba2_workspace(const Mamba2Params& p, void* ws, Mamba2Params* q);
 hipError_t launch_mamba2_scan(const Mamba2Params& p, hipStream_t stream);
 
+// ---- the layer's operators around the scans (layer_api.cpp)
+
+// Keeps the message of a failing HIP call for mssm_last_error (mssm_api.cpp).
+void set_hip_error(const char* what, hipError_t e);
+// Validates a caller's workspace: MSSM_OK or MSSM_ERR_WORKSPACE (mssm_api.cpp).
+int check_workspace(const void* ws, int64_t ws_bytes, int64_t need);
+// Compute units of the current device, cached (mssm_api.cpp).
+int compute_units();
+
+// RMS norm with the residual's addition: rows of dim; residual, residual_out
+// and rstd may be null; scales non-null: out is e4m3.
+struct NormParams {
+  const void* x;
+  const void* residual;
+  const float* weight;
+  void* out;
+  uint8_t* scales;        // (rows, scale_cols) e8m0 or null
+  void* residual_out;
+  float* rstd;
+  int64_t rows, x_stride, scale_cols;
+  int32_t dim;
+  float eps;
+  float inv_dim;          // set by the launch
+  int32_t threads;        // threads of a row, set by the launch
+};
+struct NormBwdParams {
+  const void* dout;
+  const void* r;
+  const float* weight;
+  const float* rstd;
+  const void* dresidual;  // may be null
+  void* dx;
+  void* dr;               // may be null
+  float* dw;
+  float* partial;         // workspace
+  int64_t rows;
+  int32_t dim;
+  float inv_dim;
+  int32_t threads;
+};
+int rms_norm_max_dim();
+int64_t rms_norm_bwd_workspace(int64_t rows, int dim, int cus);
+// res: 0 no residual stream, 1 bf16, 2 fp32.
+hipError_t launch_rms_norm(NormParams p, bool bf16, int res, hipStream_t st);
+hipError_t launch_rms_norm_bwd(NormBwdParams p, bool bf16, int res, int cus, hipStream_t st);
+
+struct QuantParams {
+  const void* x;
+  uint8_t* q;
+  uint8_t* scales;
+  int64_t rows, cols, x_stride;
+  int32_t square;         // one scale for each 128 x 128 block
+  int32_t transpose;      // q is (cols, rows)
+};
+hipError_t launch_quantize_fp8(const QuantParams& p, bool bf16, hipStream_t st);
+
+// out (M, N) = a (M, K) b (N, K)^T; b_rows: rows of b that share a scale.
+struct MatmulParams {
+  const uint8_t* a;
+  const uint8_t* a_scales;
+  const uint8_t* b;
+  const uint8_t* b_scales;
+  void* out;
+  int64_t M, N, K;
+  int32_t b_rows;
+};
+hipError_t launch_fp8_matmul(const MatmulParams& p, bool bf16, hipStream_t st);
+
+struct SampleParams {
+  const void* logits;
+  const float* noise;
+  int64_t* tokens;
+  float* logprobs;
+  int64_t rows, logits_stride, noise_stride;
+  int32_t vocab;
+  float temperature, top_p, min_p;
+  int32_t top_k;
+  const float* temperature_row;  // per-row settings, each may be null
+  const int32_t* top_k_row;
+  const float* top_p_row;
+  const float* min_p_row;
+};
+hipError_t launch_sample(const SampleParams& p, bool bf16, hipStream_t st);
+
+struct Mamba2StepParams {
+  float* state;           // (cache, nheads * 64, N)
+  void* conv_state;       // (cache, channels, width - 1)
+  const void* xbc;        // (batch, channels), rows xbc_stride apart
+  const void* dt;         // (batch, nheads), rows dt_stride apart
+  const void* z;          // (batch, nheads * 64), rows z_stride apart, or null
+  const float* conv_weight;
+  const float* conv_bias; // may be null
+  const float* A;
+  const float* D;         // may be null
+  const float* dt_bias;   // may be null
+  const int32_t* slots;   // (batch) rows of the states, or null
+  void* out;
+  float* u;               // workspace: (batch, channels) conv outputs
+  int64_t batch, cache, channels, xbc_stride, dt_stride, z_stride;
+  int32_t nheads, ngroups, N, width, softplus;
+};
+hipError_t launch_mamba2_step(const Mamba2StepParams& p, bool bf16, int cus, hipStream_t st);
+
 }  // namespace mssm

@@ -1,0 +1,182 @@
+"""The 8-bit quantiser and the block-scaled product, against 64-bit references."""
+import pytest
+import torch
+
+from tests import layer_common as lc
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(rows, cols, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed * 7919 + rows * 31 + cols)
+    return torch.randn(rows, cols, generator=g) * torch.exp(spread * torch.randn(cols, generator=g))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 200), (129, 127), (130, 260), (257, 16),
+                                       (64, 513)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantize(rows, cols, io, block_rows, transpose):
+    import selective_state_space_52_amd as m
+    x = rand(rows, cols, 1).to(lc.IO[io])
+    q, s = m.quantize_fp8(x.cuda(), block_rows=block_rows, transpose=transpose)
+    want_q, want_s = lc.quantize(x.t() if transpose else x, block_rows)
+    # dividing by a power of two is exact, so the values are too
+    assert torch.equal(s.view(torch.uint8).cpu(), want_s)
+    assert torch.equal(q.view(torch.uint8).cpu() & 0x7F, want_q.view(torch.uint8) & 0x7F)
+    assert torch.equal(q.cpu().double(), want_q.double())
+
+
+def test_quantize_edges():
+    import selective_state_space_52_amd as m
+    x = torch.zeros(9, 128)
+    x[1, 3], x[1, 4] = float("inf"), 2.0
+    x[2, 3], x[2, 4] = float("nan"), -448.0
+    x[3, 0] = 448.0 * 4            # largest value of scale 4
+    x[4, 0] = 448.0 * 4 + 2.0 ** -10 * 448 * 4
+    x[5, 0] = 1e-38
+    x[6, 0] = 3.4e38
+    x[7] = 1e-42                   # below the smallest normal fp32
+    x[8] = float("nan")
+    for block_rows, transpose in ((1, False), (1, True), (128, False)):
+        q, s = m.quantize_fp8((x.t().contiguous() if transpose else x).cuda(), block_rows, transpose)
+        want_q, want_s = lc.quantize(x, block_rows)
+        assert torch.equal(s.view(torch.uint8).cpu(), want_s)
+        got, want = q.float().cpu(), want_q.float()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+def test_quantize_strided():
+    import selective_state_space_52_amd as m
+    x = rand(150, 300, 4).to(torch.bfloat16).cuda()
+    for args in ((1, False), (1, True), (128, True)):
+        a, b = m.quantize_fp8(x[:, 5:205], *args), m.quantize_fp8(x[:, 5:205].contiguous(), *args)
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8))
+        assert torch.equal(a[1].view(torch.uint8), b[1].view(torch.uint8))
+
+
+def operands(M, N, K, b_rows, seed):
+    a, sa = lc.quantize(rand(M, K, seed))
+    b, sb = lc.quantize(rand(N, K, seed + 1), b_rows)
+    return a, sa, b, sb
+
+
+def check_product(got, a, sa, b, sb, b_rows, dtype):
+    aw, bw = lc.widen(a, sa), lc.widen(b, sb, b_rows)
+    want = aw @ bw.t()
+    if dtype == torch.float32:   # sums of K products in fp32
+        slack = (a.shape[1] + 4) * lc.U32 * (aw.abs() @ bw.abs().t())
+    else:
+        # the 8-bit instructions hold the products of one block to 2^-17 of the
+        # largest: K such errors of either sign, within 8 of their deviations
+        slack = 8 * 2.0 ** -17 * torch.zeros_like(want)
+        for k in range(0, a.shape[1], 128):
+            at = slice(k, k + 128)
+            big = aw[:, at].abs().amax(1)[:, None] * bw[:, at].abs().amax(1)[None]
+            slack += 8 * 2.0 ** -17 * big * min(128, a.shape[1] - k) ** 0.5
+    lc.bound(got, want, slack, dtype)
+
+
+PRODUCTS = [(1, 1, 1), (1, 16, 128), (3, 5, 7), (16, 33, 130), (17, 100, 256), (33, 129, 400),
+            (64, 257, 1037), (65, 64, 64), (100, 130, 200), (129, 257, 129), (255, 300, 1000),
+            (300, 520, 640), (513, 1000, 272)]
+
+
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("b_rows", [1, 128])
+def test_product(M, N, K, dtype, b_rows):
+    import selective_state_space_52_amd as m
+    a, sa, b, sb = operands(M, N, K, b_rows, 11)
+    got = m.fp8_matmul(a.cuda(), sa.view(lc.E8).cuda(), b.cuda(), sb.view(lc.E8).cuda(),
+                       out_dtype=dtype)
+    again = m.fp8_matmul(a.cuda(), sa.view(lc.E8).cuda(), b.cuda(), sb.view(lc.E8).cuda(),
+                         out_dtype=dtype)
+    assert torch.equal(got, again)
+    check_product(got, a, sa, b, sb, b_rows, dtype)
+
+
+@pytest.mark.parametrize("M,N", [(5, 40), (200, 300)])
+def test_product_places(M, N):
+    """Small whole numbers with scales that differ in every block: exact, so a
+    misplaced row, column or scale shows at once."""
+    import selective_state_space_52_amd as m
+    K = 700
+    g = torch.Generator().manual_seed(3)
+    a = torch.randint(-2, 3, (M, K), generator=g).float().to(lc.F8)
+    b = torch.randint(-2, 3, (N, K), generator=g).float().to(lc.F8)
+    for b_rows in (1, 128):
+        sa = torch.randint(125, 130, (M, 6), generator=g, dtype=torch.uint8)
+        sb = torch.randint(125, 130, (-(-N // b_rows), 6), generator=g, dtype=torch.uint8)
+        want = lc.widen(a, sa) @ lc.widen(b, sb, b_rows).t()
+        got = m.fp8_matmul(a.cuda(), sa.view(lc.E8).cuda(), b.cuda(), sb.view(lc.E8).cuda(),
+                           out_dtype=torch.float32)
+        assert torch.equal(got.cpu().double(), want)
+        got = m.fp8_matmul(a.cuda(), sa.view(lc.E8).cuda(), b.cuda(), sb.view(lc.E8).cuda())
+        assert torch.equal(got.cpu(), want.to(torch.bfloat16))
+
+
+def test_product_nan_stays_in_its_row():
+    import selective_state_space_52_amd as m
+    for M in (20, 150):
+        a, sa, b, sb = operands(M, 140, 300, 128, 5)
+        a[7, 290] = float("nan")
+        b[133, 3] = float("nan")
+        for dtype in (torch.bfloat16, torch.float32):
+            got = m.fp8_matmul(a.cuda(), sa.view(lc.E8).cuda(), b.cuda(), sb.view(lc.E8).cuda(),
+                               out_dtype=dtype).cpu()
+            want = torch.zeros(M, 140, dtype=torch.bool)
+            want[7], want[:, 133] = True, True
+            assert torch.equal(torch.isnan(got), want)
+
+
+def test_linear_gradients():
+    """dX and dW of a layer out = x w^T in 8 bits: the formula's with the
+    quantised operands exactly as the kernels see them, and the layer's own
+    gradients to the quantisation's precision."""
+    import selective_state_space_52_amd as m
+    M, N, K = 300, 200, 270
+    x, w, g = rand(M, K, 1, 0.3), rand(N, K, 2, 0.3) / 16, rand(M, N, 3, 0.3)
+    xd, wd, gd = (t.to(torch.bfloat16).cuda() for t in (x, w, g))
+    wt, wts = m.quantize_fp8(wd, block_rows=128, transpose=True)
+    gq, gs = m.quantize_fp8(gd)
+    dx = m.fp8_matmul(gq, gs, wt, wts)
+    gt, gts = m.quantize_fp8(gd, transpose=True)
+    xt, xts = m.quantize_fp8(xd, transpose=True)
+    dw = m.fp8_matmul(gt, gts, xt, xts, out_dtype=torch.float32)
+    check_product(dx, gq.cpu(), gs.view(torch.uint8).cpu(), wt.cpu(), wts.view(torch.uint8).cpu(), 128,
+                  torch.bfloat16)
+    check_product(dw, gt.cpu(), gts.view(torch.uint8).cpu(), xt.cpu(), xts.view(torch.uint8).cpu(), 1,
+                  torch.float32)
+    # e4m3 rounds to 2^-4 at most, about 2^-5 on average: 5% covers two operands
+    for got, want in ((dx, g.double() @ w.double()), (dw, g.double().t() @ x.double())):
+        assert float((got.cpu().double() - want).norm() / want.norm()) < 0.05
+    # differences of the loss sum(g * x w^T), linear in w: one step is exact
+    v = rand(N, K, 4, 0.0).double()
+    along = float(((x.double() @ (w.double() + v).t() - x.double() @ w.double().t()) * g.double()).sum())
+    size = float((g.double().t() @ x.double()).norm() * v.norm())
+    assert abs(float((dw.cpu().double() * v).sum()) - along) < 0.05 * size
+
+
+def test_refusals():
+    import selective_state_space_52_amd as m
+    a, sa, b, sb = (t.cuda() for t in operands(8, 8, 256, 128, 1))
+    sa, sb = sa.view(lc.E8), sb.view(lc.E8)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a.cpu(), sa, b, sb)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a.float(), sa, b, sb)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a, sa[:, :1].contiguous(), b, sb)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a, sa, b[:, :128].contiguous(), sb)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a, sa, b, sb, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        m.fp8_matmul(a, sa, b, sb.view(torch.uint8))
+    with pytest.raises(ValueError):
+        m.quantize_fp8(torch.zeros(4, 4, device="cuda"), block_rows=64)
+    with pytest.raises(m.MssmError):
+        m.quantize_fp8(torch.zeros(0, 4, device="cuda"))

@@ -1,0 +1,148 @@
+"""Sampling from given random numbers, against the definition in 64 bits."""
+import pytest
+import torch
+
+from tests import layer_common as lc
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def check(logits, noise, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, per_row=True):
+    import selective_state_space_52_amd as m
+    rows = logits.shape[0]
+
+    def wide(v, dtype):
+        return torch.as_tensor(v, dtype=dtype).expand(rows).contiguous()
+    t, k, p, q = (wide(temperature, torch.float32), wide(top_k, torch.int32),
+                  wide(top_p, torch.float32), wide(min_p, torch.float32))
+    want, want_lp = lc.sample(logits.cpu(), noise.cpu(), t, k, p, q)
+    if per_row:
+        args = dict(temperature=t.cuda(), top_k=k.cuda(), top_p=p.cuda(), min_p=q.cuda())
+    else:
+        args = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+    tokens, lp = m.sample_tokens(logits.cuda(), noise.cuda(), **args)
+    again, lp2 = m.sample_tokens(logits.cuda(), noise.cuda(), **args)
+    assert torch.equal(tokens, again) and torch.equal(lp, lp2)
+    assert tokens.tolist() == want
+    for got, ref in zip(lp.tolist(), want_lp):
+        # (l - m) / T: 3 roundings; the logarithm of a sum of hardware exponentials
+        assert got == ref or abs(got - ref) <= 2e-6 + 4 * lc.U32 * abs(ref)
+
+
+def random(rows, vocab, seed, scale=3.0, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(rows, vocab, generator=g) * scale).to(dtype), torch.rand(rows, vocab, generator=g)
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 63, 64, 1000, 1025, 4099, 50257])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", [
+    dict(), dict(temperature=0.0), dict(top_k=1), dict(top_k=7), dict(top_k=300),
+    dict(top_p=0.9), dict(top_p=0.3, temperature=1.7), dict(min_p=0.1),
+    dict(temperature=0.6, top_k=50, top_p=0.8, min_p=0.05), dict(top_k=10**6, top_p=0.999)])
+def test_settings(vocab, dtype, settings):
+    logits, noise = random(5, vocab, vocab, dtype=dtype)
+    check(logits, noise, per_row=vocab % 2 == 0, **settings)
+
+
+def test_settings_differ_by_row():
+    logits, noise = random(8, 3001, 4)
+    check(logits, noise, temperature=[0.0, 0.5, 1.0, 2.0, 1.0, 1.0, 1.0, 0.7],
+          top_k=[5, 0, 1, 40, 0, 2999, 17, 3001], top_p=[0.5, 0.9, 0.9, 1.0, 0.2, 0.99, 0.0, 0.7],
+          min_p=[0.0, 0.1, 0.0, 0.02, 2.0, 0.0, 0.0, 0.01])
+
+
+def test_one_setting_by_row():
+    import selective_state_space_52_amd as m
+    logits, noise = random(6, 500, 14)
+    k = torch.tensor([1, 2, 3, 0, 5, 600], dtype=torch.int32)
+    want, _ = lc.sample(logits, noise, [0.8] * 6, k, [0.9] * 6, [0.0] * 6)
+    tokens, _ = m.sample_tokens(logits.cuda(), noise.cuda(), temperature=0.8, top_k=k.cuda(), top_p=0.9)
+    assert tokens.tolist() == want
+
+
+@pytest.mark.parametrize("vocab", [5, 2000, 40000])
+def test_ties(vocab):
+    """Equal logits: top-k and top-p keep the lowest indices."""
+    _, noise = random(6, vocab, 5)
+    logits = torch.zeros(6, vocab)
+    logits[1:, vocab // 2:] = -1.0
+    logits[3] = -0.0
+    logits[3, ::2] = 0.0
+    check(logits, noise, top_k=[3, vocab // 2 + 2, 2, 3, 0, 0], top_p=[1.0, 1.0, 0.5, 1.0, 0.6, 0.9])
+    check(logits, noise, temperature=0.0)
+
+
+def test_masked_rows():
+    vocab = 700
+    logits, noise = random(9, vocab, 6)
+    logits[0] = -INF                        # nothing left
+    logits[1] = float("nan")
+    logits[2, 1:] = -INF                    # one token left, the first
+    logits[3, :-1] = -INF                   # and the last
+    logits[4, 100:] = -INF
+    logits[5] = torch.finfo(torch.float32).min   # a mask of the lowest value everywhere
+    logits[6, ::2] = torch.finfo(torch.float32).min
+    logits[7, 5] = logits[7, 9] = INF       # all the mass in two tokens
+    logits[8, ::3] = float("nan")
+    for s in (dict(), dict(top_k=3), dict(top_p=0.7), dict(top_k=650, top_p=0.99, min_p=0.001),
+              dict(temperature=0.0), dict(min_p=0.5)):
+        check(logits, noise, **s)
+
+
+def test_noise_at_its_ends():
+    vocab = 300
+    logits, noise = random(4, vocab, 7)
+    noise[0] = 0.0
+    noise[1, :] = 0.5
+    noise[2, 17] = 1.0
+    noise[3, ::2] = 0.0
+    check(logits, noise)
+    check(logits, noise, top_k=20)
+
+
+def test_rows_of_a_wider_matrix_and_streams():
+    import selective_state_space_52_amd as m
+    logits, noise = random(7, 1100, 8, dtype=torch.bfloat16)
+    wide, wn = logits.cuda(), noise.cuda()
+    got = m.sample_tokens(wide[:, 3:1003], wn[:, 1:1001], top_p=0.9)
+    same = m.sample_tokens(wide[:, 3:1003].contiguous(), wn[:, 1:1001].contiguous(), top_p=0.9)
+    assert torch.equal(got[0], same[0]) and torch.equal(got[1], same[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = m.sample_tokens(wide[:, 3:1003], wn[:, 1:1001], top_p=0.9)
+    side.synchronize()
+    assert torch.equal(got[0], other[0])
+
+
+def test_frequencies():
+    """Tokens are taken in proportion to their probability: 4000 draws of a
+    four-token row, each count within 5 standard deviations."""
+    import selective_state_space_52_amd as m
+    n = 4000
+    p = torch.tensor([0.5, 0.3, 0.15, 0.05])
+    noise = torch.rand(n, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    tokens, lp = m.sample_tokens(torch.log(p).expand(n, 4).contiguous().cuda(), noise)
+    count = torch.bincount(tokens.cpu(), minlength=4).double()
+    assert ((count - n * p).abs() <= 5 * torch.sqrt(n * p * (1 - p))).all()
+    assert torch.allclose(lp.cpu(), torch.log(p)[tokens.cpu()], atol=2e-6)
+
+
+def test_refusals():
+    import selective_state_space_52_amd as m
+    logits, noise = random(3, 100, 9)
+    lc_, nc = logits.cuda(), noise.cuda()
+    with pytest.raises(ValueError):
+        m.sample_tokens(logits, noise)
+    with pytest.raises(ValueError):
+        m.sample_tokens(lc_, nc[:, :50])
+    with pytest.raises(ValueError):
+        m.sample_tokens(lc_, nc.double())
+    with pytest.raises(ValueError):
+        m.sample_tokens(lc_, nc, top_k=torch.zeros(3, device="cuda"))
+    with pytest.raises(ValueError):
+        m.sample_tokens(lc_, nc, top_p=torch.ones(2, device="cuda"))
+    with pytest.raises(m.MssmError):
+        m.sample_tokens(lc_[:0], nc[:0])
