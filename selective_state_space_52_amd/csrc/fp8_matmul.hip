@@ -21,6 +21,8 @@
 // ends with neighbouring n of one m.  Both operands put the same k in the same
 // lane and register, and a whole block of 128 has one scale, so any order of
 // k inside the block gives the same sum.
+#include <type_traits>
+
 #include "fp8.h"
 #include "mssm_internal.h"
 
@@ -180,54 +182,183 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulParams p)
 //
 // A workgroup of WM x WN waves takes a BM x BN tile of out, in steps of one
 // block of 128 along k.  A step's BM + BN rows of 128 bytes are staged in LDS
-// in two buffers, the next step's loads in flight while this one's products
-// run.  A row is 8 pieces of 16 bytes; row r keeps piece c in place
+// in one of S buffers, the next S - 1 steps' loads in flight while this one's
+// products run.  A row is 8 pieces of 16 bytes; row r keeps piece c in place
 // c ^ ((r >> 1) & 7), so that the same piece of 16 neighbouring rows covers all
 // 64 banks.
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int S>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int kRows = BM + BN;           // a's rows, then b's
-  static constexpr int kFm = BM / WM / 32, kFn = BN / WN / 32;
-  static constexpr int kPieces = kRows * 8 / kThreads;  // 16-byte pieces a thread stages
+  static constexpr int kRows = BM + BN;                 // a's rows, then b's
+  static constexpr int kFm = BM / WM / 32, kFn = BN / WN / 32;  // tiles of a wave
+  static constexpr int kLoads = kRows / (8 * kWaves);   // loads of 8 rows a wave stages
+  static constexpr int kLoadsA = BM / (8 * kWaves);     // the first of them a's
+  static constexpr int kChunk = 32;                     // steps whose scales are in LDS
 };
 
 __device__ __forceinline__ int piece_at(int row, int c) {
   return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) {
-  using T = Tile<BM, BN, WM, WN>;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][T::kRows * 128];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t tiles_m = (p.M + BM - 1) / BM;
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * BM, n0 = (int64_t)(blockIdx.x / tiles_m) * BN;
-  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
-  const int64_t kbs = (p.K + kScaleBlock - 1) / kScaleBlock;
+// Tiles of out in the order in which workgroups take them.  Workgroups go
+// round the 8 XCDs, each with its own L2: XCD x takes the x-th eighth of a
+// sequence that runs down kBand rows of tiles at a time, so that the tiles in
+// flight on one XCD share few rows of a and b.
+constexpr int kXcds = 8, kBand = 4;
+// s_waitcnt: at most n vector memory operations outstanding, and no LDS one.
+constexpr int wait_loads(int n) { return (n & 15) | (n >> 4 & 3) << 14 | 0x0070; }
+// A barrier that leaves loads in flight (__syncthreads waits for them all): for
+// use after the wait for what the other waves are to see.
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n,
+                                        uint32_t* tm, uint32_t* tn) {
+  const uint32_t tiles = tiles_m * tiles_n;
+  const uint32_t x = id % kXcds, per = tiles / kXcds, rest = tiles % kXcds;
+  const uint32_t t = x * per + min(x, rest) + id / kXcds;
+  const uint32_t band = t / (kBand * tiles_n), in = t - band * kBand * tiles_n;
+  const uint32_t height = min((uint32_t)kBand, tiles_m - band * kBand);
+  *tn = in / height;
+  *tm = band * kBand + in - *tn * height;
+}
 
-  auto stage = [&](int64_t kb, uint8_t* to) {
+// Asks for a half's LDS reads between its matrix instructions.
+template <class T, int kMore>
+__device__ __forceinline__ void interleave() {
+  constexpr int kReads = 2 * (T::kFm + T::kFn) + kMore, kMul = T::kFm * T::kFn;
 #pragma unroll
-    for (int i = 0; i < T::kPieces; ++i) {
-      const int at = i * T::kThreads + threadIdx.x;
-      const int row = at >> 3, c = at & 7;
-      const bool isa = row < BM;
-      const int64_t g = isa ? m0 + row : n0 + row - BM;
-      i32x4 v = i32x4{0, 0, 0, 0};
-      if (g < (isa ? p.M : p.N))
-        v = load16((isa ? p.a : p.b) + g * p.K, kb * kScaleBlock + c * 16, p.K);
-      *reinterpret_cast<i32x4*>(to + piece_at(row, c)) = v;
+  for (int i = 0; i < kMul; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul - 1) / kMul, 0);
+  }
+}
+
+// 16 bytes of a row at column k, zeros from K on, without a branch for rows of
+// 16 bytes or more: near the end the row's last 16 bytes, shifted.
+__device__ __forceinline__ i32x4 load16_tail(const uint8_t* row, int k, int K) {
+  if (K < 16) return load16(row, k, K);
+  const int over = max(k - (K - 16), 0);
+  const Any16 a = *reinterpret_cast<const Any16*>(row + min(k, K - 16));
+  unsigned __int128 v = (unsigned __int128)a.w[3] << 96 | (unsigned __int128)a.w[2] << 64 |
+                        (unsigned __int128)a.w[1] << 32 | a.w[0];
+  v = over < 16 ? v >> (8 * over) : 0;
+  return i32x4{(int)(uint32_t)v, (int)(uint32_t)(v >> 32), (int)(uint32_t)(v >> 64),
+               (int)(uint32_t)(v >> 96)};
+}
+
+// DIRECT: rows start at multiples of 4 bytes, and buffer loads put 16 bytes a
+// lane straight into LDS, a wave 8 rows at a time in the order of the lanes
+// (the rotation of the pieces is in the lanes' addresses).  Rows past the
+// matrix are past the buffer's end and read as zeros.  A row's last bytes that
+// fill no piece are kept in registers and put in place when their step is due.
+// Otherwise every load goes through registers, written to LDS a step later.
+template <bool BF16, bool DIRECT, int BM, int BN, int WM, int WN, int S>
+__global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) {
+  using T = Tile<BM, BN, WM, WN, S>;
+  // One array for the buffers and the scales: the compiler tells two
+  // arrays' accesses apart and then waits for every load into the first before
+  // any read of it, the other buffer's too (248 us against 218 at 8192 x 10576
+  // x 2560).
+  constexpr int kBuffer = T::kRows * 128, kScalePitch = T::kChunk + 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kBuffer + T::kRows * kScalePitch];
+  uint8_t* const scale = lds + S * kBuffer;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, (uint32_t)((p.M + BM - 1) / BM), (uint32_t)((p.N + BN - 1) / BN), &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+  const int K = (int)p.K, kbs = (K + kScaleBlock - 1) / kScaleBlock;
+  const int rows_a = (int)min((int64_t)BM, p.M - m0), rows_b = (int)min((int64_t)BN, p.N - n0);
+
+  const uint8_t* const ga = p.a + m0 * K;
+  const uint8_t* const gb = p.b + n0 * K;
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(ga), 0, rows_a * K, 0x00027000);
+  const auto rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(gb), 0, rows_b * K, 0x00027000);
+  // this lane's row and piece in a wave's load of 8 rows; the rows of load i
+  // start at 8 (i * kWaves + wave), so bits 1..3 of the row do not depend on i
+  static_assert(T::kWaves % 2 == 0, "the piece's place may not depend on the load");
+  const int srow = 8 * wave + (lane >> 3);
+  const int spiece = (lane & 7) ^ ((srow >> 1) & 7);
+  const int soff = srow * K + spiece * 16;
+
+  // A thread's own row of the staged tile, for its scales and its last bytes;
+  // past the matrix the last row again, whose results go nowhere.
+  static_assert(T::kRows <= T::kThreads, "a thread takes one row's scales");
+  const int my = min((int)threadIdx.x, T::kRows - 1);
+  const int my_row = my < BM ? min(my, rows_a - 1) : min(my - BM, rows_b - 1);
+  const uint32_t nb = (uint32_t)(n0 + my_row);
+  const uint8_t* const my_scales =
+      my < BM ? p.a_scales + (m0 + my_row) * kbs
+              : p.b_scales + (int64_t)(p.b_rows == 1 ? nb : nb / kScaleBlock) * kbs;
+  const bool words = kbs % 4 == 0 && ((uintptr_t)p.a_scales | (uintptr_t)p.b_scales) % 4 == 0;
+  const bool ragged = DIRECT && K % 16 != 0;
+  i32x4 last = i32x4{0, 0, 0, 0};
+  if (ragged) last = load16((my < BM ? ga : gb) + (int64_t)my_row * K, K & ~15, K);
+
+  i32x4 held[DIRECT ? 1 : T::kLoads];
+  auto load = [&](int kb, uint8_t* to) {
+    if constexpr (DIRECT) {
+      // a piece past the last column, or with it inside: past the buffer's end
+      const bool in = kb * kScaleBlock + spiece * 16 + 16 <= K;
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) {
+        const bool isa = i < T::kLoadsA;
+        const int off = soff + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves) * K;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            isa ? ra : rb,
+            (__attribute__((address_space(3))) void*)(to + (i * T::kWaves + wave) * 1024), 16,
+            in ? off : 0x7FFFFFF0, kb * kScaleBlock, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i) {
+        const bool isa = i < T::kLoadsA;
+        // rows past the matrix: the last one again, whose results go nowhere
+        const int row = min(srow + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves),
+                            (isa ? rows_a : rows_b) - 1);
+        held[i] = load16_tail((isa ? ga : gb) + (int64_t)row * K, kb * kScaleBlock + spiece * 16, K);
+      }
+    }
+  };
+  auto put = [&](uint8_t* to) {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int i = 0; i < T::kLoads; ++i)
+        *reinterpret_cast<i32x4*>(to + (i * T::kWaves + wave) * 1024 + lane * 16) = held[i];
     }
   };
 
-  const uint8_t* as[T::kFm];
-  const uint8_t* bs[T::kFn];
+  auto put_last = [&](uint8_t* to) {
+    if (threadIdx.x < T::kRows)
+      *reinterpret_cast<i32x4*>(to + piece_at(threadIdx.x, (K & 127) >> 4)) = last;
+  };
+
+  // The scales of a chunk of steps, one row of bytes for each row of the
+  // staged tile: a thread reads a row's from memory, and a lane its bytes from
+  // LDS.  (A byte a lane straight from memory touches 32 lines an
+  // instruction: 230 us against 218.)
+  auto load_scales = [&](int c0, int n) {
+    uint32_t w[T::kChunk / 4];
 #pragma unroll
-  for (int i = 0; i < T::kFm; ++i)
-    as[i] = p.a_scales + min(m0 + wm + 32 * i + (lane & 31), p.M - 1) * kbs;
+    for (int q = 0; q < T::kChunk / 4; ++q) {
+      if (words) {  // past the chunk's end: its last word again
+        w[q] = *reinterpret_cast<const uint32_t*>(my_scales + c0 + (min(4 * q, n - 1) & ~3));
+      } else {
+        w[q] = 0;
 #pragma unroll
-  for (int j = 0; j < T::kFn; ++j)
-    bs[j] = p.b_scales + min(n0 + wn + 32 * j + (lane & 31), p.N - 1) / p.b_rows * kbs;
+        for (int e = 0; e < 4; ++e)
+          w[q] |= (uint32_t)my_scales[c0 + min(4 * q + e, n - 1)] << (8 * e);
+      }
+    }
+    if (threadIdx.x < T::kRows)
+#pragma unroll
+      for (int q = 0; q < T::kChunk / 4; ++q)
+        *reinterpret_cast<uint32_t*>(scale + threadIdx.x * kScalePitch + 4 * q) = w[q];
+  };
 
   f32x16 acc[T::kFm][T::kFn];
 #pragma unroll
@@ -237,94 +368,203 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
 
-  stage(0, lds[0]);
-  __syncthreads();
-  for (int64_t kb = 0; kb < kbs; ++kb) {
-    if (kb + 1 < kbs) stage(kb + 1, lds[(kb + 1) & 1]);
-    const uint8_t* at = lds[kb & 1];
-    int sa[T::kFm], sb[T::kFn];
+  // Half a step's operands: 64 of the 128 columns.
+  struct Half {
+    Frag a[T::kFm], b[T::kFn];
+  };
+  const int arow = wm + (lane & 31), brow = BM + wn + (lane & 31);
+  auto read = [&](Half& f, const uint8_t* at, int h) {
+    const int c = 4 * h + 2 * (lane >> 5);
 #pragma unroll
-    for (int i = 0; i < T::kFm; ++i) sa[i] = as[i][kb];
+    for (int q = 0; q < 2; ++q) {
 #pragma unroll
-    for (int j = 0; j < T::kFn; ++j) sb[j] = bs[j][kb];
+      for (int i = 0; i < T::kFm; ++i)
+        f.a[i].h[q] = *reinterpret_cast<const i32x4*>(at + piece_at(arow + 32 * i, c + q));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Frag a[T::kFm], b[T::kFn];
-      const int c = 4 * h + 2 * (lane >> 5);
+      for (int j = 0; j < T::kFn; ++j)
+        f.b[j].h[q] = *reinterpret_cast<const i32x4*>(at + piece_at(brow + 32 * j, c + q));
+    }
+  };
+  int sa[T::kFm], sb[T::kFn];
+  auto multiply = [&](const Half& f) {
+    if constexpr (BF16) {
 #pragma unroll
-      for (int i = 0; i < T::kFm; ++i) {
-        const int row = wm + 32 * i + (lane & 31);
-        a[i].h[0] = *reinterpret_cast<const i32x4*>(at + piece_at(row, c));
-        a[i].h[1] = *reinterpret_cast<const i32x4*>(at + piece_at(row, c + 1));
-      }
+      for (int i = 0; i < T::kFm; ++i)
 #pragma unroll
-      for (int j = 0; j < T::kFn; ++j) {
-        const int row = BM + wn + 32 * j + (lane & 31);
-        b[j].h[0] = *reinterpret_cast<const i32x4*>(at + piece_at(row, c));
-        b[j].h[1] = *reinterpret_cast<const i32x4*>(at + piece_at(row, c + 1));
-      }
-      if constexpr (BF16) {
+        for (int j = 0; j < T::kFn; ++j)
+          acc[i][j] = mfma32(f.b[j], f.a[i], acc[i][j], sb[j], sa[i]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x8 aw[T::kFm], bw[T::kFn];
+#pragma unroll
+        for (int i = 0; i < T::kFm; ++i) aw[i] = widen8(f.a[i], q, scale_value(sa[i]));
+#pragma unroll
+        for (int j = 0; j < T::kFn; ++j) bw[j] = widen8(f.b[j], q, scale_value(sb[j]));
 #pragma unroll
         for (int i = 0; i < T::kFm; ++i)
 #pragma unroll
-          for (int j = 0; j < T::kFn; ++j) acc[i][j] = mfma32(b[j], a[i], acc[i][j], sb[j], sa[i]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bf16x8 aw[T::kFm], bw[T::kFn];
-#pragma unroll
-          for (int i = 0; i < T::kFm; ++i) aw[i] = widen8(a[i], q, scale_value(sa[i]));
-#pragma unroll
-          for (int j = 0; j < T::kFn; ++j) bw[j] = widen8(b[j], q, scale_value(sb[j]));
-#pragma unroll
-          for (int i = 0; i < T::kFm; ++i)
-#pragma unroll
-            for (int j = 0; j < T::kFn; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j], aw[i], acc[i][j], 0, 0, 0);
-        }
+          for (int j = 0; j < T::kFn; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j], aw[i], acc[i][j], 0, 0, 0);
       }
     }
+  };
+  auto read_scales = [&](int (&ta)[T::kFm], int (&tb)[T::kFn], int k) {
+#pragma unroll
+    for (int i = 0; i < T::kFm; ++i) ta[i] = scale[(arow + 32 * i) * kScalePitch + k];
+#pragma unroll
+    for (int j = 0; j < T::kFn; ++j) tb[j] = scale[(brow + 32 * j) * kScalePitch + k];
+  };
+
+  // Each half's operands are read while the half before it is multiplied.  In
+  // the middle of a step, when its second half has been read by every wave,
+  // its buffer takes the step S after it.
+  Half f0, f1;
+  int next_sa[T::kFm], next_sb[T::kFn];
+  for (int c0 = 0; c0 < kbs; c0 += T::kChunk) {
+    const int n = min(T::kChunk, kbs - c0);
+    const int due = ragged ? kbs - 1 - c0 : -1;  // the step that takes the rows' last bytes
+    load_scales(c0, n);
+    load(c0, lds);
+    put(lds);
+    // past the last step: zeros that no one reads
+#pragma unroll
+    for (int q = 1; q < (DIRECT ? S : 2); ++q) load(c0 + q, lds + q * kBuffer);
+    __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 1) * T::kLoads : 0));
+    if (due == 0) put_last(lds);
+    __syncthreads();
+    read(f0, lds, 0);
+    read_scales(sa, sb, 0);
+    uint8_t* here = lds;
+    for (int k = 0; k + 1 < n; ++k) {
+      uint8_t* const there = here == lds + (S - 1) * kBuffer ? lds : here + kBuffer;
+      __builtin_amdgcn_sched_barrier(0);
+      read(f1, here, 1);
+      multiply(f0);
+      interleave<T, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      // the next step's loads are done (a wave's loads into LDS count as its
+      // vector memory, in order, and every step has kLoads of them), and this
+      // wave's reads of this step
+      put(there);
+      if (k + 1 == due) {  // after the zeros that the loads put there
+        __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 2) * T::kLoads : 0));
+        barrier();
+        put_last(there);
+      }
+      __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 2) * T::kLoads : 0));
+      barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      load(c0 + k + (DIRECT ? S : 2), here);
+      read(f0, there, 0);
+      read_scales(next_sa, next_sb, k + 1);
+      multiply(f1);
+      interleave<T, T::kFm + T::kFn>();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < T::kFm; ++i) sa[i] = next_sa[i];
+#pragma unroll
+      for (int j = 0; j < T::kFn; ++j) sb[j] = next_sb[j];
+      here = there;
+    }
+    read(f1, here, 1);
+    multiply(f0);
+    multiply(f1);
+    // the loads past the last step still write to LDS
+    __builtin_amdgcn_s_waitcnt(wait_loads(0));
     __syncthreads();
   }
+
+  // The tile goes out through LDS, 32 rows of a wave's tile at a time, so that
+  // a store covers whole lines of a row.
+  using Out = typename std::conditional<BF16, uint16_t, float>::type;
+  constexpr int kWn = BN / WN, kPer = 16 / sizeof(Out);  // columns of a wave; of one store
+  constexpr int kPitch = kWn * sizeof(Out) + 16;
+  static_assert(T::kWaves * 32 * kPitch <= S * kBuffer, "the results fit in the staging buffers");
+  uint8_t* const mine = lds + wave * 32 * kPitch;
+  const int left_m = rows_a - wm, left_n = rows_b - wn;
+  Out* const out = static_cast<Out*>(p.out) + (m0 + wm) * p.N + n0 + wn;
 #pragma unroll
   for (int i = 0; i < T::kFm; ++i) {
-    const int64_t m = m0 + wm + 32 * i + (lane & 31);
-    if (m >= p.M) continue;
 #pragma unroll
     for (int j = 0; j < T::kFn; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + wn + 32 * j + 8 * q + 4 * (lane >> 5);
-        if (n < p.N)
-          store4<BF16>(p.out, m * p.N + n, (int)min((int64_t)4, p.N - n), acc[i][j][4 * q],
-                       acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        const f32x16& v = acc[i][j];
+        uint8_t* to = mine + (lane & 31) * kPitch + (32 * j + 8 * q + 4 * (lane >> 5)) * sizeof(Out);
+        if constexpr (BF16)
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                                                     pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+        else
+          *reinterpret_cast<float4*>(to) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
+    __builtin_amdgcn_wave_barrier();  // a wave's LDS operations keep their order
+#pragma unroll
+    for (int k = 0; k < 32 * kWn / kPer / 64; ++k) {
+      const int at = k * 64 + lane, r = at / (kWn / kPer), c = at % (kWn / kPer) * kPer;
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + r * kPitch + c * sizeof(Out));
+      const int row = 32 * i + r, n = left_n - c;
+      Out* const to = out + row * p.N + c;
+      if (row >= left_m || n <= 0) continue;
+      if (n >= kPer) {
+        *reinterpret_cast<Any16*>(to) = Any16{{v.x, v.y, v.z, v.w}};
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (e < n)
+            to[e] = BF16 ? (Out)(w[e / 2 % 4] >> (16 * (e & 1))) : (Out)__uint_as_float(w[e % 4]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN>
+template <bool BF16, int BM, int BN, int WM, int WN, int S>
 void launch_tile(const MatmulParams& p, hipStream_t st) {
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((fp8_tile_kernel<BF16, BM, BN, WM, WN>), dim3((unsigned)tiles),
-                     dim3(64 * WM * WN), 0, st, p);
+  const dim3 grid((unsigned)tiles), block(64 * WM * WN);
+  if (p.K % 4 == 0 && ((uintptr_t)p.a | (uintptr_t)p.b) % 4 == 0)
+    hipLaunchKernelGGL((fp8_tile_kernel<BF16, true, BM, BN, WM, WN, S>), grid, block, 0, st, p);
+  else
+    hipLaunchKernelGGL((fp8_tile_kernel<BF16, false, BM, BN, WM, WN, S>), grid, block, 0, st, p);
 }
 
+// The tile by how many of them there are: the largest that still occupies most
+// of the compute units.  Measured, us (M x N x K; the tiles from left to right
+// are those of the branches below, top to bottom):
+//   8192 x 10576 x 2560   227   273   324   390
+//   2048 x 2560 x 5120     49    34    46    50
+//   1024 x 2560 x 5120     48    33    23    32
+//   128 x 2560 x 5120      45    33    23    14
+// An fp32 output takes twice the matrix instructions and its operands'
+// widening, and stops at 128 x 128.
 template <bool BF16>
-void launch(const MatmulParams& p, hipStream_t st) {
-  if (p.M <= 64) {
+void launch(const MatmulParams& p, int cus, hipStream_t st) {
+  const auto tiles = [&](int64_t bm, int64_t bn) {
+    return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+  };
+  if (p.M <= 32) {
     const dim3 grid((unsigned)((p.N + 15) / 16)), block(64 * kFewWaves);
     if (p.M <= 16) hipLaunchKernelGGL((fp8_few_kernel<BF16, 1>), grid, block, 0, st, p);
-    else if (p.M <= 32) hipLaunchKernelGGL((fp8_few_kernel<BF16, 2>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((fp8_few_kernel<BF16, 4>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((fp8_few_kernel<BF16, 2>), grid, block, 0, st, p);
     return;
   }
-  launch_tile<BF16, 128, 128, 2, 2>(p, st);
+  if constexpr (BF16) {
+    if (8 * tiles(192, 256) >= 7 * cus) return launch_tile<BF16, 192, 256, 2, 4, 2>(p, st);
+    if (2 * tiles(128, 256) >= cus) return launch_tile<BF16, 128, 256, 2, 4, 3>(p, st);
+    if (8 * tiles(128, 128) >= 5 * cus) return launch_tile<BF16, 128, 128, 2, 4, 4>(p, st);
+  } else {
+    if (8 * tiles(128, 128) >= 5 * cus) return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
+  }
+  launch_tile<BF16, 64, 64, 2, 2, 4>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_matmul(const MatmulParams& p, bool bf16, hipStream_t st) {
-  bf16 ? launch<true>(p, st) : launch<false>(p, st);
+hipError_t launch_fp8_matmul(const MatmulParams& p, bool bf16, int cus, hipStream_t st) {
+  bf16 ? launch<true>(p, cus, st) : launch<false>(p, cus, st);
   return hipGetLastError();
 }
 

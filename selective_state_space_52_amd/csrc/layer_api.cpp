@@ -231,7 +231,8 @@ int mssm_fp8_matmul(const void* a, const void* a_scales, const void* b, const vo
   const mssm::MatmulParams p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scales),
                              static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scales),
                              out, M, N, K, dims->b_block_rows};
-  return done(mssm::launch_fp8_matmul(p, dims->out_dtype == MSSM_BF16, (hipStream_t)stream),
+  return done(mssm::launch_fp8_matmul(p, dims->out_dtype == MSSM_BF16, mssm::compute_units(),
+                                      (hipStream_t)stream),
               "fp8 product launch");
 }
 

@@ -339,7 +339,7 @@ struct MatmulParams {
   int64_t M, N, K;
   int32_t b_rows;
 };
-hipError_t launch_fp8_matmul(const MatmulParams& p, bool bf16, hipStream_t st);
+hipError_t launch_fp8_matmul(const MatmulParams& p, bool bf16, int cus, hipStream_t st);
 
 struct SampleParams {
   const void* logits;
