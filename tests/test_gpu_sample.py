@@ -35,12 +35,14 @@ def random(rows, vocab, seed, scale=3.0, dtype=torch.float32):
     return (torch.randn(rows, vocab, generator=g) * scale).to(dtype), torch.rand(rows, vocab, generator=g)
 
 
-@pytest.mark.parametrize("vocab", [1, 2, 63, 64, 1000, 1025, 4099, 50257])
+@pytest.mark.parametrize("vocab", [1, 2, 63, 64, 1000, 1025, 4099, 20011, 50257, 70001])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("settings", [
     dict(), dict(temperature=0.0), dict(top_k=1), dict(top_k=7), dict(top_k=300),
     dict(top_p=0.9), dict(top_p=0.3, temperature=1.7), dict(min_p=0.1),
-    dict(temperature=0.6, top_k=50, top_p=0.8, min_p=0.05), dict(top_k=10**6, top_p=0.999)])
+    dict(temperature=0.6, top_k=50, top_p=0.8, min_p=0.05), dict(top_k=10**6, top_p=0.999),
+    dict(top_k=900, top_p=0.9, temperature=2.0), dict(top_k=3500, top_p=0.6, temperature=3.0),
+    dict(top_k=5000, min_p=0.001), dict(top_p=0.99, temperature=50.0), dict(top_p=0.8, temperature=0.02)])
 def test_settings(vocab, dtype, settings):
     logits, noise = random(5, vocab, vocab, dtype=dtype)
     check(logits, noise, per_row=vocab % 2 == 0, **settings)
@@ -62,7 +64,7 @@ def test_one_setting_by_row():
     assert tokens.tolist() == want
 
 
-@pytest.mark.parametrize("vocab", [5, 2000, 40000])
+@pytest.mark.parametrize("vocab", [5, 2000, 40000, 80000])
 def test_ties(vocab):
     """Equal logits: top-k and top-p keep the lowest indices."""
     _, noise = random(6, vocab, 5)
