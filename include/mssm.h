@@ -616,7 +616,9 @@ typedef struct {
  *                outside [0, cache) marks padding: its out is zero and no
  *                state is touched.  No two sequences may share a row.
  *   out        : (batch, nheads * headdim) io dtype
- * The convolution's output stays in fp32.
+ * The convolution's output stays in fp32.  One launch; the workspace holds
+ * counters that the caller clears once, before its first use, and that every
+ * call leaves at zero.
  */
 int mssm_mamba2_state_update(float* state, void* conv_state, const void* xbc, const void* dt,
                              const float* conv_weight, const float* conv_bias, const float* A,

@@ -273,7 +273,7 @@ int mssm_mamba2_state_update_workspace(const mssm_step_dims* dims, int64_t* byte
   if (!bytes) return MSSM_ERR_NULL;
   const int rc = check_step_dims(dims);
   if (rc != MSSM_OK) return rc;
-  *bytes = dims->batch * (dims->nheads * 64 + 2 * dims->ngroups * dims->dstate) * 4;
+  *bytes = dims->batch * dims->ngroups * 4;
   return MSSM_OK;
 }
 
@@ -312,7 +312,7 @@ int mssm_mamba2_state_update(float* state, void* conv_state, const void* xbc, co
   std::memset(&p, 0, sizeof(p));
   p.state = state; p.conv_state = conv_state; p.xbc = xbc; p.dt = dt; p.z = z;
   p.conv_weight = conv_weight; p.conv_bias = conv_bias; p.A = A; p.D = D; p.dt_bias = dt_bias;
-  p.slots = slots; p.out = out; p.u = static_cast<float*>(workspace);
+  p.slots = slots; p.out = out; p.counters = static_cast<uint32_t*>(workspace);
   p.batch = batch; p.cache = dims->cache; p.channels = ch;
   p.xbc_stride = xs; p.dt_stride = ds; p.z_stride = zs;
   p.nheads = (int32_t)H; p.ngroups = (int32_t)dims->ngroups; p.N = (int32_t)N;

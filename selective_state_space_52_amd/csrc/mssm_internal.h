@@ -370,7 +370,7 @@ struct Mamba2StepParams {
   const float* dt_bias;   // may be null
   const int32_t* slots;   // (batch) rows of the states, or null
   void* out;
-  float* u;               // workspace: (batch, channels) conv outputs
+  uint32_t* counters;     // workspace: (batch, ngroups), zero before and after
   int64_t batch, cache, channels, xbc_stride, dt_stride, z_stride;
   int32_t nheads, ngroups, N, width, softplus;
 };

@@ -55,34 +55,56 @@ def _refuse(t, name, dtype, shape, device):
 
 
 def _io(t, name, dims):
-    if t.dtype not in _IO:
+    io = _IO.get(t.dtype)
+    if io is None:
         raise ValueError("%s must be float32 or bfloat16" % name)
     if t.dim() != dims:
         raise ValueError("%s must have %d dimensions" % (name, dims))
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
-    return _IO[t.dtype]
+    return io
+
+
+# The current device and its current stream's handle, without the Stream object
+# that torch.cuda.current_stream makes (2 us of a small call's 14).
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(device, fn, *args):
     """fn(*args, current stream of the device), checked."""
     index = device.index
-    if index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        check(rc)
 
 
-def _workspace(device, size_fn, dims):
-    """A workspace of a call (from torch's caching allocator, so ordered on the
-    current stream) and its 256-byte aligned address."""
+def _size(fn, dims, device):
+    """Bytes of workspace that a call on this device needs."""
     n = ctypes.c_int64(0)
-    with torch.cuda.device(device):
-        check(size_fn(dims, ctypes.byref(n)))
-    buf = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
-    p = buf.data_ptr()
-    return buf, p + (-p) % 256, n.value
+    if device.index == _current_device():
+        check(fn(dims, n))
+    else:
+        with torch.cuda.device(device):
+            check(fn(dims, n))
+    return n.value
+
+
+# The step's counters, one buffer for each (device, stream), on which calls run
+# in order: cleared when it is made, left at zero by every call.
+_COUNTERS = {}
+
+
+def _counters(device, need):
+    key = (device.index, _raw_stream(device.index))
+    buf = _COUNTERS.get(key)
+    if buf is None or buf.numel() * 4 < need:
+        buf = _COUNTERS[key] = torch.zeros(max(1024, need // 4), dtype=torch.int32, device=device)
+    return buf
 
 
 def _norm(x, weight, residual, eps, want_rstd, fp8):
@@ -153,9 +175,11 @@ def rms_norm_bwd(dout, r, weight, rstd, dresidual=None):
     dx = torch.empty_like(dout)
     dw = torch.empty(dim, dtype=torch.float32, device=dev)
     dims = NormDims(rows, dim, 0, io, res, 0.0, 0)
-    buf, ws, nws = _workspace(dev, lib().mssm_rms_norm_bwd_workspace, dims)
+    need = _size(lib().mssm_rms_norm_bwd_workspace, dims, dev)
+    # from torch's caching allocator: ordered on the current stream, 512-byte aligned
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call(dev, lib().mssm_rms_norm_bwd, _ptr(dout), _ptr(r), _ptr(weight), _ptr(rstd),
-          _ptr(dresidual), _ptr(dx), _ptr(dr), _ptr(dw), ws, nws, dims, int(has))
+          _ptr(dresidual), _ptr(dx), _ptr(dr), _ptr(dw), _ptr(ws), need, dims, int(has))
     return dx, dr, dw
 
 
@@ -286,8 +310,9 @@ def mamba2_state_update(state, conv_state, xbc, dt, conv_weight, A, conv_bias=No
     else:
         _is(out, "out", dtype, (batch, dim), dev)
     dims = StepDims(batch, cache, heads, 64, ngroups, N, *strides, width, io)
-    buf, ws, nws = _workspace(dev, lib().mssm_mamba2_state_update_workspace, dims)
+    need = batch * ngroups * 4
+    ws = _counters(dev, need)
     _call(dev, lib().mssm_mamba2_state_update, _ptr(state), _ptr(conv_state), _ptr(xbc), _ptr(dt),
           _ptr(conv_weight), _ptr(conv_bias), _ptr(A), _ptr(D), _ptr(z), _ptr(dt_bias),
-          int(bool(softplus)), _ptr(slots), _ptr(out), ws, nws, dims)
+          int(bool(softplus)), _ptr(slots), _ptr(out), _ptr(ws), need, dims)
     return out
