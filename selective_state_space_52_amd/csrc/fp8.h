@@ -44,36 +44,37 @@ __device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float 
 struct __attribute__((packed, aligned(1))) Any8 { uint32_t w[2]; };
 struct __attribute__((packed, aligned(1))) Any16 { uint32_t w[4]; };
 
-// v[0..7] = p[i..i+7], the values past `n` of them zero.
+// v[0..7] = p[i..i+7], the values past `n` >= 1 of them zero.  (Written without
+// loops: an array filled in loops of two branches was put into scratch memory.)
 template <bool BF16>
 __device__ __forceinline__ void load8(float (&v)[8], const void* p, int64_t i, int n) {
+  uint32_t w0, w1, w2, w3, w4, w5, w6, w7;
   if constexpr (BF16) {
     const uint16_t* q = static_cast<const uint16_t*>(p) + i;
     if (n >= 8) {
       const Any16 a = *reinterpret_cast<const Any16*>(q);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16_lo(a.w[j]);
-        v[2 * j + 1] = bf16_hi(a.w[j]);
-      }
+      w0 = a.w[0], w1 = a.w[1], w2 = a.w[2], w3 = a.w[3];
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < n ? bf16_bits(q[j]) : 0.0f;
+      const auto at = [&](int j) { return j < n ? (uint32_t)q[min(j, n - 1)] : 0u; };
+      w0 = at(0) | at(1) << 16, w1 = at(2) | at(3) << 16;
+      w2 = at(4) | at(5) << 16, w3 = at(6);
     }
+    v[0] = bf16_lo(w0), v[1] = bf16_hi(w0), v[2] = bf16_lo(w1), v[3] = bf16_hi(w1);
+    v[4] = bf16_lo(w2), v[5] = bf16_hi(w2), v[6] = bf16_lo(w3), v[7] = bf16_hi(w3);
   } else {
-    const float* q = static_cast<const float*>(p) + i;
+    const uint32_t* q = static_cast<const uint32_t*>(p) + i;
     if (n >= 8) {
       const Any16 a = reinterpret_cast<const Any16*>(q)[0];
       const Any16 b = reinterpret_cast<const Any16*>(q)[1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = __uint_as_float(a.w[j]);
-        v[4 + j] = __uint_as_float(b.w[j]);
-      }
+      w0 = a.w[0], w1 = a.w[1], w2 = a.w[2], w3 = a.w[3];
+      w4 = b.w[0], w5 = b.w[1], w6 = b.w[2], w7 = b.w[3];
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < n ? q[j] : 0.0f;
+      const auto at = [&](int j) { return j < n ? q[min(j, n - 1)] : 0u; };
+      w0 = at(0), w1 = at(1), w2 = at(2), w3 = at(3), w4 = at(4), w5 = at(5), w6 = at(6), w7 = 0;
     }
+    v[0] = __uint_as_float(w0), v[1] = __uint_as_float(w1), v[2] = __uint_as_float(w2);
+    v[3] = __uint_as_float(w3), v[4] = __uint_as_float(w4), v[5] = __uint_as_float(w5);
+    v[6] = __uint_as_float(w6), v[7] = __uint_as_float(w7);
   }
 }
 

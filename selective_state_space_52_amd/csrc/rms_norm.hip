@@ -188,22 +188,26 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_bwd_kernel(NormBwdParams
   }
 }
 
-// The second launch: dw[i] = sum of the partial rows, in their order.  A
-// workgroup takes 32 columns, each of its 16 half-waves every 16th row.
-__global__ void __launch_bounds__(512) rms_norm_dw_kernel(const float* __restrict__ partial,
-                                                          float* __restrict__ dw, int dim,
-                                                          int rows) {
-  __shared__ float lds[16][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+// The second launch: dw[i] = sum of the partial rows, in a fixed order.  A
+// workgroup takes 16 columns, each of its 64 groups of 16 threads every 64th row.
+constexpr int kDwCols = 16, kDwGroups = 64;
+__global__ void __launch_bounds__(kDwCols* kDwGroups)
+    rms_norm_dw_kernel(const float* __restrict__ partial, float* __restrict__ dw, int dim, int rows) {
+  __shared__ float lds[kDwGroups][kDwCols + 1];
+  const int c = threadIdx.x % kDwCols, part = threadIdx.x / kDwCols;
+  const int col = blockIdx.x * kDwCols + c;
   float s = 0.0f;
-  if (col < dim)
-    for (int r = part; r < rows; r += 16) s += partial[(int64_t)r * dim + col];
-  lds[part][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (part == 0 && col < dim) {
-    for (int q = 1; q < 16; ++q) s += lds[q][threadIdx.x];
-    dw[col] = s;
+  if (col < dim) {
+#pragma unroll 8
+    for (int r = part; r < rows; r += kDwGroups) s += partial[(int64_t)r * dim + col];
   }
+  lds[part][c] = s;
+  __syncthreads();
+  for (int half = kDwGroups / 2; half > 0; half /= 2) {
+    if (part < half) lds[part][c] += lds[part + half][c];
+    __syncthreads();
+  }
+  if (part == 0 && col < dim) dw[col] = lds[0][c];
 }
 
 struct Shape {
@@ -265,7 +269,7 @@ hipError_t launch_rms_norm(NormParams p, bool bf16, int res, hipStream_t st) {
 // Workgroups of the backward's first launch.
 static int64_t bwd_blocks(int64_t rows, Shape s, int cus) {
   const int64_t per = s.threads == 64 ? s.block / 64 : 1;
-  const int64_t resident = (int64_t)cus * (2048 / s.block > 4 ? 4 : 2048 / s.block);
+  const int64_t resident = (int64_t)cus * (s.block >= 512 ? 2 : 1024 / s.block);
   const int64_t need = (rows + per - 1) / per;
   return need < resident ? need : resident;
 }
@@ -290,8 +294,8 @@ hipError_t launch_rms_norm_bwd(NormBwdParams p, bool bf16, int res, int cus, hip
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int parts = (int)(blocks * (s.threads == 64 ? s.block / 64 : 1));
-  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((p.dim + 31) / 32)), dim3(512), 0, st,
-                     p.partial, p.dw, p.dim, parts);
+  hipLaunchKernelGGL(rms_norm_dw_kernel, dim3((unsigned)((p.dim + kDwCols - 1) / kDwCols)),
+                     dim3(kDwCols * kDwGroups), 0, st, p.partial, p.dw, p.dim, parts);
   return hipGetLastError();
 }
 
