@@ -82,6 +82,19 @@ __device__ __forceinline__ i32x4 load16(const uint8_t* row, int64_t k, int64_t K
   return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
+// 16 bytes of a row at column k, zeros from K on, without a branch for rows of
+// 16 bytes or more: near the end the row's last 16 bytes, shifted.
+__device__ __forceinline__ i32x4 load16_tail(const uint8_t* row, int k, int K) {
+  if (K < 16) return load16(row, k, K);
+  const int over = max(k - (K - 16), 0);
+  const Any16 a = *reinterpret_cast<const Any16*>(row + min(k, K - 16));
+  unsigned __int128 v = (unsigned __int128)a.w[3] << 96 | (unsigned __int128)a.w[2] << 64 |
+                        (unsigned __int128)a.w[1] << 32 | a.w[0];
+  v = over < 16 ? v >> (8 * over) : 0;
+  return i32x4{(int)(uint32_t)v, (int)(uint32_t)(v >> 32), (int)(uint32_t)(v >> 64),
+               (int)(uint32_t)(v >> 96)};
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store4(void* out, int64_t at, int n, float a, float b, float c,
                                        float d) {
@@ -111,54 +124,78 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int n, float a, fl
 //
 // A workgroup takes 16 rows of b and all of a's rows (MT tiles of 16); its 8
 // waves take every 8th block of 128, straight from memory into the
-// instruction's registers, and their sums meet in LDS.  b is read once: its
-// bytes bound the kernel.
+// instruction's registers, up to kAhead blocks a turn, and their sums meet in
+// LDS.  b is read once; a's rows come from L2 to every workgroup, in as many
+// loads as b's, and the loads' addresses bound the kernel (16 x 10576 x 2560:
+// 10.1 us, 2.7 TB/s of b; 7.8 us for one row of a).  Holding all four blocks'
+// loads ahead of the first product costs the registers of half the waves: 14.1
+// us.
 constexpr int kFewWaves = 8;
 
-template <bool BF16, int MT>
+// WHOLE: rows of whole, aligned 16 bytes.
+template <bool BF16, bool WHOLE, int MT>
 __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulParams p) {
+  constexpr int kAhead = MT == 1 ? 4 : 2;
   __shared__ float part[kFewWaves][MT][64][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t kbs = (p.K + kScaleBlock - 1) / kScaleBlock;
+  const int K = (int)p.K, kbs = (K + kScaleBlock - 1) / kScaleBlock;
   // rows past the last read the last one; what they give is not stored
   const int64_t nr = min(n0 + (lane & 15), p.N - 1);
-  const uint8_t* brow = p.b + nr * p.K;
-  const uint8_t* bs = p.b_scales + (nr / p.b_rows) * kbs;
+  const uint8_t* brow = p.b + nr * K;
+  const uint8_t* bs = p.b_scales + (p.b_rows == 1 ? nr : (int64_t)((uint32_t)nr / kScaleBlock)) * kbs;
   const uint8_t* arow[MT];
   const uint8_t* as[MT];
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t m = min((int64_t)i * 16 + (lane & 15), p.M - 1);
-    arow[i] = p.a + m * p.K;
+    arow[i] = p.a + m * K;
     as[i] = p.a_scales + m * kbs;
     acc[i] = f32x4{0, 0, 0, 0};
   }
-  for (int64_t kb = wave; kb < kbs; kb += kFewWaves) {
-    const int64_t k = kb * kScaleBlock + (lane >> 4) * 32;
-    Frag b, a[MT];
-    b.h[0] = load16(brow, k, p.K);
-    b.h[1] = load16(brow, k + 16, p.K);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      a[i].h[0] = load16(arow[i], k, p.K);
-      a[i].h[1] = load16(arow[i], k + 16, p.K);
-    }
-    const int sb = bs[kb];
-    if constexpr (BF16) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = mfma16(b, a[i], acc[i], sb, as[i][kb]);
+  const auto piece = [&](const uint8_t* row, int k) {
+    if constexpr (WHOLE) {
+      // a piece past the end: the row's last, whose products are with zeros
+      const i32x4 v = *reinterpret_cast<const i32x4*>(row + min(k, K - 16));
+      return k < K ? v : i32x4{0, 0, 0, 0};
     } else {
-      float sa[MT];
+      return load16_tail(row, k, K);
+    }
+  };
+  for (int kb0 = wave; kb0 < kbs; kb0 += kAhead * kFewWaves) {
+    Frag b[kAhead], a[kAhead][MT];
+    int sb[kAhead], sa[kAhead][MT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) sa[i] = scale_value(as[i][kb]);
+    for (int q = 0; q < kAhead; ++q) {
+      const int kb = min(kb0 + q * kFewWaves, kbs - 1);
+      // a quarter of each half of the block, so that four lanes read 64 bytes
+      const int k = kb * kScaleBlock + (lane >> 4) * 16;
+      b[q].h[0] = piece(brow, k);
+      b[q].h[1] = piece(brow, k + 64);
+      sb[q] = bs[kb];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bf16x8 bw = widen8(b, q, scale_value(sb));
+      for (int i = 0; i < MT; ++i) {
+        a[q][i].h[0] = piece(arow[i], k);
+        a[q][i].h[1] = piece(arow[i], k + 64);
+        sa[q][i] = as[i][kb];
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw, widen8(a[i], q, sa[i]), acc[i], 0, 0, 0);
+    for (int q = 0; q < kAhead; ++q) {
+      if (kb0 + q * kFewWaves >= kbs) break;
+      if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = mfma16(b[q], a[q][i], acc[i], sb[q], sa[q][i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bf16x8 bw = widen8(b[q], e, scale_value(sb[q]));
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                bw, widen8(a[q][i], e, scale_value(sa[q][i])), acc[i], 0, 0, 0);
+        }
       }
     }
   }
@@ -234,19 +271,6 @@ __device__ __forceinline__ void interleave() {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul - 1) / kMul, 0);
   }
-}
-
-// 16 bytes of a row at column k, zeros from K on, without a branch for rows of
-// 16 bytes or more: near the end the row's last 16 bytes, shifted.
-__device__ __forceinline__ i32x4 load16_tail(const uint8_t* row, int k, int K) {
-  if (K < 16) return load16(row, k, K);
-  const int over = max(k - (K - 16), 0);
-  const Any16 a = *reinterpret_cast<const Any16*>(row + min(k, K - 16));
-  unsigned __int128 v = (unsigned __int128)a.w[3] << 96 | (unsigned __int128)a.w[2] << 64 |
-                        (unsigned __int128)a.w[1] << 32 | a.w[0];
-  v = over < 16 ? v >> (8 * over) : 0;
-  return i32x4{(int)(uint32_t)v, (int)(uint32_t)(v >> 32), (int)(uint32_t)(v >> 64),
-               (int)(uint32_t)(v >> 96)};
 }
 
 // DIRECT: rows start at multiples of 4 bytes, and buffer loads put 16 bytes a
@@ -547,8 +571,14 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
   };
   if (p.M <= 32) {
     const dim3 grid((unsigned)((p.N + 15) / 16)), block(64 * kFewWaves);
-    if (p.M <= 16) hipLaunchKernelGGL((fp8_few_kernel<BF16, 1>), grid, block, 0, st, p);
-    else hipLaunchKernelGGL((fp8_few_kernel<BF16, 2>), grid, block, 0, st, p);
+    const bool whole = p.K % 16 == 0 && ((uintptr_t)p.a | (uintptr_t)p.b) % 16 == 0;
+    if (p.M <= 16) {
+      if (whole) hipLaunchKernelGGL((fp8_few_kernel<BF16, true, 1>), grid, block, 0, st, p);
+      else hipLaunchKernelGGL((fp8_few_kernel<BF16, false, 1>), grid, block, 0, st, p);
+    } else {
+      if (whole) hipLaunchKernelGGL((fp8_few_kernel<BF16, true, 2>), grid, block, 0, st, p);
+      else hipLaunchKernelGGL((fp8_few_kernel<BF16, false, 2>), grid, block, 0, st, p);
+    }
     return;
   }
   if constexpr (BF16) {
