@@ -449,7 +449,8 @@ int mssm_set_scan_timing_events(void* start, void* stop);
  * choice of the next token.  Memory, streams and errors are as above; these
  * calls allocate nothing, and those that need a workspace take it from the
  * caller (256-byte aligned, of the size that the call's _workspace function
- * gives for the device that is current).
+ * gives for the device that is current).  Sizes whose launch would need 2^32
+ * threads or more are refused (MSSM_ERR_DIMS).
  *
  * 8-bit values are e4m3 (1 sign, 4 exponent and 3 mantissa bits, largest value
  * 448, no infinity).  Each block of 128 of them has a scale that is a power of

@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMost = INT64_MAX / 16;  // elements of one array
 constexpr int64_t kGrid = INT32_MAX;       // workgroups of one launch
+constexpr int64_t kItems = UINT32_MAX;     // threads of one launch
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
@@ -63,6 +64,7 @@ int check_norm_dims(const mssm_norm_dims* d) {
   if (d->rows <= 0 || d->dim <= 0 || d->rows > kGrid || !fits(d->rows, d->dim))
     return MSSM_ERR_DIMS;
   if (d->dim > mssm::rms_norm_max_dim()) return MSSM_ERR_UNSUPPORTED;
+  if (!fits(d->rows, (d->dim / 8 + 256) / 64 * 64, kItems)) return MSSM_ERR_DIMS;
   if (d->x_stride != 0 && (d->x_stride < d->dim || !fits(d->rows, d->x_stride)))
     return MSSM_ERR_DIMS;
   return MSSM_OK;
@@ -109,12 +111,12 @@ int check_step_dims(const mssm_step_dims* d) {
   if (d->headdim != 64 || (d->dstate != 64 && d->dstate != 128) || d->width < 2 || d->width > 4 ||
       d->nheads % d->ngroups != 0)
     return MSSM_ERR_UNSUPPORTED;
-  // one launch covers the heads' pieces (at most 8) and the channels
+  // a head, or half of one, a workgroup
   if (!fits(d->nheads, 64, INT32_MAX / 8) || !fits(d->ngroups, 2 * d->dstate, INT32_MAX / 8) ||
-      !fits(d->batch, d->nheads * 8, kGrid))
+      !fits(d->batch, d->nheads * 2, kItems / 256))
     return MSSM_ERR_DIMS;
   const int64_t channels = d->nheads * 64 + 2 * d->ngroups * d->dstate;
-  if (!fits(d->batch, channels, kGrid * 256) || !fits(d->cache, channels, kMost / 4) ||
+  if (!fits(d->batch, channels) || !fits(d->cache, channels, kMost / 4) ||
       !fits(d->cache, d->nheads * 64 * d->dstate))
     return MSSM_ERR_DIMS;
   const int64_t least[3] = {channels, d->nheads, d->nheads * 64};
@@ -197,7 +199,7 @@ int mssm_quantize_fp8(const void* x, void* q, void* scales, const mssm_quant_dim
   const bool square = dims->block_rows == 128, t = dims->transpose != 0;
   const bool rowwise = !square && !t;
   const int64_t nb = rowwise ? rows * blocks128(cols) / 16 : blocks128(rows) * blocks128(cols);
-  if (nb >= kGrid) return MSSM_ERR_DIMS;
+  if (nb >= kItems / 512) return MSSM_ERR_DIMS;
   if (!x || !q || !scales) return MSSM_ERR_NULL;
   const int64_t io = size_of(dims->io_dtype);
   if (!aligned(x, io)) return MSSM_ERR_ALIGN;
@@ -219,7 +221,7 @@ int mssm_fp8_matmul(const void* a, const void* a_scales, const void* b, const vo
     return MSSM_ERR_UNSUPPORTED;
   const int64_t M = dims->m, N = dims->n, K = dims->k;
   if (!fits(M, N) || !fits(M, K) || !fits(N, K) || K > (1 << 22) ||
-      (M + 63) / 64 > kGrid / ((N + 63) / 64) || N / 16 >= kGrid)
+      (M + 63) / 64 > kItems / 256 / ((N + 63) / 64) || N / 16 >= kItems / 512)
     return MSSM_ERR_DIMS;
   if (!a || !a_scales || !b || !b_scales || !out) return MSSM_ERR_NULL;
   const int64_t size = size_of(dims->out_dtype);
@@ -243,7 +245,7 @@ int mssm_sample(const void* logits, const float* noise, int64_t* tokens, float* 
   const int64_t rows = args->rows, V = args->vocab;
   const int64_t ls = args->logits_stride ? args->logits_stride : V;
   const int64_t ns = args->noise_stride ? args->noise_stride : V;
-  if (rows <= 0 || V <= 0 || rows > kGrid || V > (1 << 22) || ls < V || ns < V ||
+  if (rows <= 0 || V <= 0 || rows > kItems / 1024 || V > (1 << 22) || ls < V || ns < V ||
       !fits(rows, ls) || !fits(rows, ns))
     return MSSM_ERR_DIMS;
   if (!logits || !noise || !tokens || !logprobs) return MSSM_ERR_NULL;

@@ -165,12 +165,12 @@ struct Weight {
     return (uint32_t)__builtin_rintf(v * kUnits);
   }
   // The same without the look at the largest logit, which `scaled` needs where
-  // that or 1 / T is infinite.
+  // that is infinite, or 1 / T nearly.
   __device__ __forceinline__ float fast(float x) const {
     return hw_exp2((x - max) * (inv_t * kLog2e));
   }
   __device__ __forceinline__ bool plain() const {
-    return fabsf(max) <= 3.402823466e38f && inv_t <= 3.402823466e38f;
+    return fabsf(max) <= 3.402823466e38f && inv_t <= 2e38f;
   }
 };
 
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleParams p) {
   const uint64_t win = block.reduce(
       score >= 0.0f ? entry_of(__float_as_uint(score), winner) : 0, Max());
   if (t == 0) {
-    const int token = index_of(win);
+    const int token = index_of(win);  // some token is always kept
     p.tokens[r] = token;
     p.logprobs[r] = w.scaled(logit<BF16>(row.row, token)) - hw_log2((float)kept) * kLn2;
   }

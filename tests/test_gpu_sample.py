@@ -104,6 +104,22 @@ def test_noise_at_its_ends():
     check(logits, noise, top_k=20)
 
 
+@pytest.mark.parametrize("temperature", [1e-45, 3e-39, 1e-30, 1e30, INF, float("nan")])
+def test_extreme_temperatures(temperature):
+    """Down to the smallest temperature only the largest logits have mass; at the
+    largest every finite one has the same."""
+    import selective_state_space_52_amd as m
+    logits, noise = random(3, 900, 21)
+    logits[1, 5:9] = logits[1].max() + 1
+    logits[2, ::2] = -INF
+    for s in (dict(), dict(top_k=20), dict(top_p=0.7), dict(top_k=700, top_p=0.5)):
+        tokens, lp = m.sample_tokens(logits.cuda(), noise.cuda(), temperature=temperature, **s)
+        tokens, lp = tokens.cpu(), lp.cpu()
+        assert (torch.gather(logits, 1, tokens[:, None]) > -INF).all() and torch.isfinite(lp).all()
+        if not temperature > 1:
+            assert torch.equal(torch.gather(logits, 1, tokens[:, None])[:, 0], logits.max(1).values)
+
+
 def test_rows_of_a_wider_matrix_and_streams():
     import selective_state_space_52_amd as m
     logits, noise = random(7, 1100, 8, dtype=torch.bfloat16)
