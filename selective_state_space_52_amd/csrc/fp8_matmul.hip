@@ -571,7 +571,9 @@ void launch_tile(const MatmulParams& p, hipStream_t st) {
 //   1024 x 2560 x 5120     48    33    23    32
 //   128 x 2560 x 5120      45    33    23    14
 // An fp32 output takes twice the matrix instructions and its operands'
-// widening, and stops at 128 x 128.
+// widening, and stops at 128 x 128; with fewer than two of those for each CU,
+// 128 x 64 or 64 x 64 (3352 x 768 x 4096: 36, 33, 36; 8192 x 10576 x 2560:
+// 408, 483, 601).
 template <bool BF16>
 void launch(const MatmulParams& p, int cus, hipStream_t st) {
   const auto tiles = [&](int64_t bm, int64_t bn) {
@@ -594,7 +596,8 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
     if (2 * tiles(128, 256) >= cus) return launch_tile<BF16, 128, 256, 2, 4, 3>(p, st);
     if (8 * tiles(128, 128) >= 5 * cus) return launch_tile<BF16, 128, 128, 2, 4, 4>(p, st);
   } else {
-    if (8 * tiles(128, 128) >= 5 * cus) return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
+    if (tiles(128, 128) >= 2 * cus) return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
+    if (tiles(128, 64) >= cus) return launch_tile<BF16, 128, 64, 2, 2, 2>(p, st);
   }
   launch_tile<BF16, 64, 64, 2, 2, 4>(p, st);
 }

@@ -7,8 +7,8 @@
 // The division is by a power of two, so each value is rounded once.  An
 // infinity becomes NaN; it and NaN leave the block's scale alone.  The
 // kernels read and write each value once: HBM bounds large ones (4096 x 3352
-// bf16: along rows 8 us, 5 TB/s; transposed 14 us, where the columns' maxima and
-// the turn through LDS wait for the whole tile).
+// bf16: along rows 8 us, 5 TB/s; transposed 12 us, 15 with the workgroups in row
+// order).
 #include "fp8.h"
 #include "mssm_internal.h"
 
@@ -41,22 +41,26 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(QuantParams p) {
   if ((threadIdx.x & 15) == 0) p.scales[block] = (uint8_t)code;
 }
 
-// A 128 x 128 tile a workgroup: thread (r, g) holds rows 4r..4r+3 of columns
+// A tile of 128 rows a workgroup: thread (r, g) holds rows 4r..4r+3 of columns
 // 8g..8g+7, so that four rows of a column pack into one word of the
 // transposed tile, which is turned in LDS.  A pitch of 33 words puts the 8 x 8
 // lanes of a wave's store on 64 banks.
-// SQUARE: one scale for the tile, else one for each of its columns.
+// SQUARE: 128 columns and one scale for them all; else 64, a scale for each.
 template <bool BF16, bool SQUARE, bool TRANSPOSE>
-__global__ void __launch_bounds__(512) quant_tile_kernel(QuantParams p) {
-  constexpr int kPitch = 33;
-  __shared__ float part[8][kScaleBlock];
-  __shared__ uint32_t tile[TRANSPOSE ? kScaleBlock * kPitch : 1];
-  // lanes: 8 column groups by 8 row groups; waves: 2 by 4
+__global__ void __launch_bounds__(SQUARE ? 512 : 256) quant_tile_kernel(QuantParams p) {
+  constexpr int kPitch = 33, kWide = SQUARE ? 2 : 1, kCols = 64 * kWide;
+  __shared__ float part[8][kCols];
+  __shared__ uint32_t tile[TRANSPOSE ? kCols * kPitch : 1];
+  // lanes: 8 column groups by 8 row groups; waves: kWide by 4
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = (lane & 7) + 8 * (wave & 1), r = (lane >> 3) + 8 * (wave >> 1);
-  const int64_t tiles_c = (p.cols + kScaleBlock - 1) / kScaleBlock;
-  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-  const int64_t row0 = tr * kScaleBlock, col0 = tc * kScaleBlock;
+  const int g = (lane & 7) + 8 * (wave % kWide), r = (lane >> 3) + 8 * (wave / kWide);
+  // down the columns first where the output is transposed: workgroups side by
+  // side would write at multiples of the row count, often of the same channel
+  const int64_t tiles_c = (p.cols + kCols - 1) / kCols;
+  const int64_t tall = (p.rows + kScaleBlock - 1) / kScaleBlock;
+  const int64_t tr = TRANSPOSE ? blockIdx.x % tall : blockIdx.x / tiles_c;
+  const int64_t tc = TRANSPOSE ? blockIdx.x / tall : blockIdx.x - tr * tiles_c;
+  const int64_t row0 = tr * kScaleBlock, col0 = tc * kCols;
   const int64_t row = row0 + 4 * r, col = col0 + 8 * g;
   const int n = (int)min((int64_t)8, p.cols - col);
   float v[4][8], amax[8];
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(512) quant_tile_kernel(QuantParams p) {
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int d = 8; d < 64; d *= 2) amax[j] = fmaxf(amax[j], __shfl_xor(amax[j], d));
-      if (lane < 8) part[wave >> 1][8 * g + j] = amax[j];
+      if (lane < 8) part[wave / kWide][8 * g + j] = amax[j];
     }
     __syncthreads();
 #pragma unroll
@@ -107,14 +111,13 @@ __global__ void __launch_bounds__(512) quant_tile_kernel(QuantParams p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i][j] *= inv;
   }
-  const int64_t tiles_r = (p.rows + kScaleBlock - 1) / kScaleBlock;
   if constexpr (SQUARE) {
     if (threadIdx.x == 0)
-      p.scales[TRANSPOSE ? tc * tiles_r + tr : (int64_t)blockIdx.x] = (uint8_t)code[0];
+      p.scales[TRANSPOSE ? tc * tall + tr : (int64_t)blockIdx.x] = (uint8_t)code[0];
   } else if (r == 0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) p.scales[(col + j) * tiles_r + tr] = (uint8_t)code[j];
+      if (j < n) p.scales[(col + j) * tall + tr] = (uint8_t)code[j];
   }
   if constexpr (!TRANSPOSE) {
 #pragma unroll
@@ -128,10 +131,10 @@ __global__ void __launch_bounds__(512) quant_tile_kernel(QuantParams p) {
     for (int j = 0; j < 8; ++j)
       tile[(8 * g + j) * kPitch + r] = pack_fp8x4(v[0][j], v[1][j], v[2][j], v[3][j]);
     __syncthreads();
-    // 128 columns of 8 16-byte pieces, two a thread
+    // 8 16-byte pieces a column, two a thread
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int c = (threadIdx.x >> 3) + 64 * k, piece = threadIdx.x & 7;
+      const int c = (threadIdx.x >> 3) + kCols / 2 * k, piece = threadIdx.x & 7;
       const int64_t at = row0 + 16 * piece;
       const int left = (int)min((int64_t)16, p.rows - at);
       if (col0 + c >= p.cols || left <= 0) continue;
@@ -153,12 +156,13 @@ __global__ void __launch_bounds__(512) quant_tile_kernel(QuantParams p) {
 template <bool BF16>
 void launch(const QuantParams& p, hipStream_t st) {
   const int64_t kb = (p.cols + kScaleBlock - 1) / kScaleBlock;
-  const int64_t tiles = kb * ((p.rows + kScaleBlock - 1) / kScaleBlock);
+  const int64_t tall = (p.rows + kScaleBlock - 1) / kScaleBlock;
+  const int64_t tiles = kb * tall, halves = tall * ((p.cols + 63) / 64);
   if (!p.square && !p.transpose)
     hipLaunchKernelGGL((quant_rows_kernel<BF16>), dim3((unsigned)((p.rows * kb + 15) / 16)),
                        dim3(256), 0, st, p);
   else if (!p.square)
-    hipLaunchKernelGGL((quant_tile_kernel<BF16, false, true>), dim3((unsigned)tiles), dim3(512), 0,
+    hipLaunchKernelGGL((quant_tile_kernel<BF16, false, true>), dim3((unsigned)halves), dim3(256), 0,
                        st, p);
   else if (p.transpose)
     hipLaunchKernelGGL((quant_tile_kernel<BF16, true, true>), dim3((unsigned)tiles), dim3(512), 0,
