@@ -336,6 +336,8 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
     if constexpr (DIRECT) {
       // a piece past the last column, or with it inside: past the buffer's end
       const bool in = kb * kScaleBlock + spiece * 16 + 16 <= K;
+      // (no step past K: the address is compared with the end less the step)
+      const int step = min(kb * kScaleBlock, K);
 #pragma unroll
       for (int i = 0; i < T::kLoads; ++i) {
         const bool isa = i < T::kLoadsA;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             isa ? ra : rb,
             (__attribute__((address_space(3))) void*)(to + (i * T::kWaves + wave) * 1024), 16,
-            in ? off : 0x7FFFFFF0, kb * kScaleBlock, 0, 0);
+            in ? off : 0x7FFFFFF0, step, 0, 0);
       }
     } else {
 #pragma unroll
