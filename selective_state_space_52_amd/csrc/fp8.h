@@ -41,6 +41,7 @@ __device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float 
 // Wide accesses at any element's alignment: the type's alignment of 1 lets
 // the compiler use one global access of its full width, which gfx950 takes at
 // every byte address.
+struct __attribute__((packed, aligned(1))) Any4 { uint32_t w; };
 struct __attribute__((packed, aligned(1))) Any8 { uint32_t w[2]; };
 struct __attribute__((packed, aligned(1))) Any16 { uint32_t w[4]; };
 

@@ -21,6 +21,7 @@
 // ends with neighbouring n of one m.  Both operands put the same k in the same
 // lane and register, and a whole block of 128 has one scale, so any order of
 // k inside the block gives the same sum.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8.h"
@@ -224,13 +225,14 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulParams p)
 // c ^ ((r >> 1) & 7), so that the same piece of 16 neighbouring rows covers all
 // 64 banks.
 //
-// 8192 x 10576 x 2560 in bf16: 218 to 240 us from card to card (1.85 to 2.03
-// PFLOP/s; a large library product reaches 2.8, at this size 1.9).  A step of
-// a 192 x 256 tile takes 1.1 us against 0.65 of its matrix instructions: the
-// loads' round trips bound it (issued later in the step: 254 us), and LDS holds
-// no third buffer of this tile; smaller tiles with three move more bytes (273
-// us).  Of the rest, 1806 tiles on 256 CUs take 8 rounds for 7.05, and first
-// loads and stores about 4 us a round.
+// What bounds it, in bf16: random operands hold the clock at 1.7 to 1.9 GHz where
+// nothing but matrix instructions runs (3.3 to 3.9 PFLOP/s; 5.0 with zeros), so
+// the bytes that a product moves through LDS cost clock as well as time.  A
+// wave's own tile decides those: 128 x 128 of a 256 x 256 one, by four waves,
+// reads a byte of LDS for 128 operations, 96 x 64 of a 192 x 256 one, by eight,
+// for 77: 2.48 against 2.20 PFLOP/s at 8192 x 8192 x 8192.  Of the rest, a tile's
+// first loads and its stores take about 3 us.  The next step's loads issued
+// later in a step cost 7%.
 template <int BM, int BN, int WM, int WN, int S>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
@@ -239,6 +241,7 @@ struct Tile {
   static constexpr int kLoads = kRows / (8 * kWaves);   // loads of 8 rows a wave stages
   static constexpr int kLoadsA = BM / (8 * kWaves);     // the first of them a's
   static constexpr int kChunk = 32;                     // steps whose scales are in LDS
+  static constexpr int kLds = kRows * (128 * S + kChunk + 4);
 };
 
 __device__ __forceinline__ int piece_at(int row, int c) {
@@ -247,8 +250,8 @@ __device__ __forceinline__ int piece_at(int row, int c) {
 
 // Tiles of out in the order in which workgroups take them.  Workgroups go
 // round the 8 XCDs, each with its own L2: XCD x takes the x-th eighth of a
-// sequence that runs down kBand rows of tiles at a time, so that the tiles in
-// flight on one XCD share few rows of a and b.
+// sequence (place_of) that runs down kBand rows of tiles at a time (tile_at), so
+// that the tiles in flight on one XCD share few rows of a and b.
 constexpr int kXcds = 8, kBand = 4;
 // s_waitcnt: at most n vector memory operations outstanding, and no LDS one.
 constexpr int wait_loads(int n) { return (n & 15) | (n >> 4 & 3) << 14 | 0x0070; }
@@ -259,11 +262,12 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n,
+__device__ __forceinline__ uint32_t place_of(uint32_t id, uint32_t count) {
+  const uint32_t x = id % kXcds, per = count / kXcds, rest = count % kXcds;
+  return x * per + min(x, rest) + id / kXcds;
+}
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t tiles_n,
                                         uint32_t* tm, uint32_t* tn) {
-  const uint32_t tiles = tiles_m * tiles_n;
-  const uint32_t x = id % kXcds, per = tiles / kXcds, rest = tiles % kXcds;
-  const uint32_t t = x * per + min(x, rest) + id / kXcds;
   const uint32_t band = t / (kBand * tiles_n), in = t - band * kBand * tiles_n;
   const uint32_t height = min((uint32_t)kBand, tiles_m - band * kBand);
   *tn = in / height;
@@ -287,21 +291,18 @@ __device__ __forceinline__ void interleave() {
 // matrix are past the buffer's end and read as zeros.  A row's last bytes that
 // fill no piece are kept in registers and put in place when their step is due.
 // Otherwise every load goes through registers, written to LDS a step later.
+// `lds` holds the buffers, then the scales.  It is one array: the compiler tells
+// two arrays' accesses apart and then waits for every load into the first before
+// any read of it, the other buffer's too (248 us against 218 at 8192 x 10576 x
+// 2560).
 template <bool BF16, bool DIRECT, int BM, int BN, int WM, int WN, int S>
-__global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) {
+__device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, int64_t n0,
+                                             uint8_t* lds) {
   using T = Tile<BM, BN, WM, WN, S>;
-  // One array for the buffers and the scales: the compiler tells two
-  // arrays' accesses apart and then waits for every load into the first before
-  // any read of it, the other buffer's too (248 us against 218 at 8192 x 10576
-  // x 2560).
   constexpr int kBuffer = T::kRows * 128, kScalePitch = T::kChunk + 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kBuffer + T::kRows * kScalePitch];
   uint8_t* const scale = lds + S * kBuffer;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, (uint32_t)((p.M + BM - 1) / BM), (uint32_t)((p.N + BN - 1) / BN), &tm, &tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
   const int K = (int)p.K, kbs = (K + kScaleBlock - 1) / kScaleBlock;
   const int rows_a = (int)min((int64_t)BM, p.M - m0), rows_b = (int)min((int64_t)BN, p.N - n0);
@@ -317,19 +318,21 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
   const int spiece = (lane & 7) ^ ((srow >> 1) & 7);
   const int soff = srow * K + spiece * 16;
 
-  // A thread's own row of the staged tile, for its scales and its last bytes;
+  // A thread's own rows of the staged tile, for their scales and last bytes;
   // past the matrix the last row again, whose results go nowhere.
-  static_assert(T::kRows <= T::kThreads, "a thread takes one row's scales");
-  const int my = min((int)threadIdx.x, T::kRows - 1);
-  const int my_row = my < BM ? min(my, rows_a - 1) : min(my - BM, rows_b - 1);
-  const uint32_t nb = (uint32_t)(n0 + my_row);
-  const uint8_t* const my_scales =
-      my < BM ? p.a_scales + (m0 + my_row) * kbs
-              : p.b_scales + (int64_t)(p.b_rows == 1 ? nb : nb / kScaleBlock) * kbs;
-  const bool words = kbs % 4 == 0 && ((uintptr_t)p.a_scales | (uintptr_t)p.b_scales) % 4 == 0;
+  constexpr int kOwn = (T::kRows + T::kThreads - 1) / T::kThreads;
+  const auto own = [&](int q) { return (int)threadIdx.x + q * T::kThreads; };
+  const auto own_row = [&](int at) {
+    return at < BM ? min(at, rows_a - 1) : min(at - BM, rows_b - 1);
+  };
   const bool ragged = DIRECT && K % 16 != 0;
-  i32x4 last = i32x4{0, 0, 0, 0};
-  if (ragged) last = load16((my < BM ? ga : gb) + (int64_t)my_row * K, K & ~15, K);
+  i32x4 last[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    last[q] = i32x4{0, 0, 0, 0};
+    const int at = min(own(q), T::kRows - 1);
+    if (ragged) last[q] = load16((at < BM ? ga : gb) + (int64_t)own_row(at) * K, K & ~15, K);
+  }
 
   i32x4 held[DIRECT ? 1 : T::kLoads];
   auto load = [&](int kb, uint8_t* to) {
@@ -367,31 +370,49 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
   };
 
   auto put_last = [&](uint8_t* to) {
-    if (threadIdx.x < T::kRows)
-      *reinterpret_cast<i32x4*>(to + piece_at(threadIdx.x, (K & 127) >> 4)) = last;
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q)
+      if (own(q) < T::kRows)
+        *reinterpret_cast<i32x4*>(to + piece_at(own(q), (K & 127) >> 4)) = last[q];
   };
 
   // The scales of a chunk of steps, one row of bytes for each row of the
-  // staged tile: a thread reads a row's from memory, and a lane its bytes from
-  // LDS.  (A byte a lane straight from memory touches 32 lines an
-  // instruction: 230 us against 218.)
-  auto load_scales = [&](int c0, int n) {
-    uint32_t w[T::kChunk / 4];
+  // staged tile: a thread reads its rows' from memory, ahead of the first loads,
+  // and a lane its bytes from LDS.  (A byte a lane straight from memory touches
+  // 32 lines an instruction: 230 us against 218 at 8192 x 10576 x 2560.)
+  uint32_t words[kOwn][T::kChunk / 4];
+  auto load_scales = [&](int c0) {
 #pragma unroll
-    for (int q = 0; q < T::kChunk / 4; ++q) {
-      if (words) {  // past the chunk's end: its last word again
-        w[q] = *reinterpret_cast<const uint32_t*>(my_scales + c0 + (min(4 * q, n - 1) & ~3));
-      } else {
-        w[q] = 0;
+    for (int o = 0; o < kOwn; ++o) {
+      const int at = min(own(o), T::kRows - 1), row = own_row(at);
+      const uint32_t nb = (uint32_t)(n0 + row);
+      const uint8_t* const from =
+          at < BM ? p.a_scales + (m0 + row) * kbs
+                  : p.b_scales + (int64_t)(p.b_rows == 1 ? nb : nb / kScaleBlock) * kbs;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[q] |= (uint32_t)my_scales[c0 + min(4 * q + e, n - 1)] << (8 * e);
+      for (int q = 0; q < T::kChunk / 4; ++q) {
+        const int k = c0 + 4 * q;
+        if (kbs >= 4) {  // near the row's end its last four, moved down
+          words[o][q] = reinterpret_cast<const Any4*>(from + min(k, kbs - 4))->w;
+        } else {
+          words[o][q] = 0;
+#pragma unroll
+          for (int e = 0; e < 3; ++e)
+            words[o][q] |= (uint32_t)from[min(k + e, kbs - 1)] << (8 * e);
+        }
       }
     }
-    if (threadIdx.x < T::kRows)
+  };
+  auto put_scales = [&](int c0) {
 #pragma unroll
-      for (int q = 0; q < T::kChunk / 4; ++q)
-        *reinterpret_cast<uint32_t*>(scale + threadIdx.x * kScalePitch + 4 * q) = w[q];
+    for (int o = 0; o < kOwn; ++o)
+      if (own(o) < T::kRows)
+#pragma unroll
+        for (int q = 0; q < T::kChunk / 4; ++q) {
+          const int over = kbs >= 4 ? min(max(c0 + 4 * q - (kbs - 4), 0), 3) : 0;
+          *reinterpret_cast<uint32_t*>(scale + own(o) * kScalePitch + 4 * q) =
+              words[o][q] >> (8 * over);
+        }
   };
 
   f32x16 acc[T::kFm][T::kFn];
@@ -458,12 +479,16 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
   for (int c0 = 0; c0 < kbs; c0 += T::kChunk) {
     const int n = min(T::kChunk, kbs - c0);
     const int due = ragged ? kbs - 1 - c0 : -1;  // the step that takes the rows' last bytes
-    load_scales(c0, n);
+    load_scales(c0);
+    __builtin_amdgcn_sched_barrier(0);
     load(c0, lds);
-    put(lds);
     // past the last step: zeros that no one reads
 #pragma unroll
-    for (int q = 1; q < (DIRECT ? S : 2); ++q) load(c0 + q, lds + q * kBuffer);
+    for (int q = 1; q < (DIRECT ? S : 1); ++q) load(c0 + q, lds + q * kBuffer);
+    __builtin_amdgcn_sched_barrier(0);
+    put_scales(c0);
+    put(lds);
+    if constexpr (!DIRECT) load(c0 + 1, lds);
     __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 1) * T::kLoads : 0));
     if (due == 0) put_last(lds);
     __syncthreads();
@@ -555,23 +580,63 @@ __global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) 
   }
 }
 
+template <bool BF16, bool DIRECT, int BM, int BN, int WM, int WN, int S>
+__global__ void __launch_bounds__(64 * WM * WN) fp8_tile_kernel(MatmulParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<BM, BN, WM, WN, S>::kLds];
+  const uint32_t tiles_m = (uint32_t)((p.M + BM - 1) / BM), tiles_n = (uint32_t)((p.N + BN - 1) / BN);
+  uint32_t tm, tn;
+  tile_at(place_of(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, &tm, &tn);
+  tile_product<BF16, DIRECT, BM, BN, WM, WN, S>(p, (int64_t)tm * BM, (int64_t)tn * BN, lds);
+}
+
+// The first `whole` tiles of 256 x 256, the others in quarters: where few are
+// left for the last round, each of their quarters finds a CU of its own.
+__global__ void __launch_bounds__(256) fp8_quartered_kernel(MatmulParams p, uint32_t whole) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<256, 256, 2, 2, 2>::kLds];
+  static_assert(Tile<128, 128, 2, 2, 4>::kLds <= sizeof(lds), "a quarter fits as well");
+  const uint32_t tiles_m = (uint32_t)((p.M + 255) / 256), tiles_n = (uint32_t)((p.N + 255) / 256);
+  uint32_t tm, tn;
+  if (blockIdx.x < whole) {
+    tile_at(place_of(blockIdx.x, whole), tiles_m, tiles_n, &tm, &tn);
+    tile_product<true, true, 256, 256, 2, 2, 2>(p, (int64_t)tm * 256, (int64_t)tn * 256, lds);
+  } else {
+    const uint32_t at = place_of(blockIdx.x - whole, 4 * (tiles_m * tiles_n - whole));
+    tile_at(whole + at / 4, tiles_m, tiles_n, &tm, &tn);
+    const int64_t m0 = (int64_t)tm * 256 + (at & 1) * 128, n0 = (int64_t)tn * 256 + (at & 2) * 64;
+    if (m0 >= p.M || n0 >= p.N) return;
+    tile_product<true, true, 128, 128, 2, 2, 4>(p, m0, n0, lds);
+  }
+}
+
+bool direct(const MatmulParams& p) {
+  return p.K % 4 == 0 && ((uintptr_t)p.a | (uintptr_t)p.b) % 4 == 0;
+}
+
 template <bool BF16, int BM, int BN, int WM, int WN, int S>
 void launch_tile(const MatmulParams& p, hipStream_t st) {
   const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
   const dim3 grid((unsigned)tiles), block(64 * WM * WN);
-  if (p.K % 4 == 0 && ((uintptr_t)p.a | (uintptr_t)p.b) % 4 == 0)
+  if (direct(p))
     hipLaunchKernelGGL((fp8_tile_kernel<BF16, true, BM, BN, WM, WN, S>), grid, block, 0, st, p);
   else
     hipLaunchKernelGGL((fp8_tile_kernel<BF16, false, BM, BN, WM, WN, S>), grid, block, 0, st, p);
 }
 
-// The tile by how many of them there are: the largest that still occupies most
-// of the compute units.  Measured, us (M x N x K; the tiles from left to right
-// are those of the branches below, top to bottom):
-//   8192 x 10576 x 2560   227   273   324   390
-//   2048 x 2560 x 5120     49    34    46    50
-//   1024 x 2560 x 5120     48    33    23    32
-//   128 x 2560 x 5120      45    33    23    14
+// The tile by the rounds in which the compute units work through them.  A full
+// round of 256 x 256 being 100, one of 192 x 256 takes 68, of 128 x 256 60, of 128 x
+// 128 37, quarters too (8192 x 10576 x 2560: 42, 29, 25 and 15 us).  Measured, us (M
+// x N x K; in brackets what is taken):
+//                       256 in quarters  192 x 256  128 x 256  128 x 128  64 x 64
+//   8192 x  8192 x 8192     [446]           498
+//   8192 x 10576 x 2560     [222]           230        273        324        390
+//   4096 x 10576 x 2560      119           [111]
+//   4096 x  4096 x 4096      [58]            77
+//   4096 x  2560 x 5120       68            [51]
+//   2048 x  2560 x 5120                      49        [34]        46         50
+//   1024 x  2560 x 5120                      48         33        [23]        32
+//    128 x  2560 x 5120                      45         33         23        [14]
+// Through registers, rows of 256 x 256 tiles need more than there are (8192 x
+// 10576 x 2561: 885 us; 192 x 256: 652).
 // An fp32 output takes twice the matrix instructions and its operands'
 // widening, and stops at 128 x 128; with fewer than two of those for each CU,
 // 128 x 64 or 64 x 64 (3352 x 768 x 4096: 36, 33, 36; 8192 x 10576 x 2560:
@@ -581,6 +646,7 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
   const auto tiles = [&](int64_t bm, int64_t bn) {
     return ((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
   };
+  const auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
   if (p.M <= 32) {
     const dim3 grid((unsigned)((p.N + 15) / 16)), block(64 * kFewWaves);
     const bool whole = p.K % 16 == 0 && ((uintptr_t)p.a | (uintptr_t)p.b) % 16 == 0;
@@ -594,9 +660,21 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
     return;
   }
   if constexpr (BF16) {
-    if (8 * tiles(192, 256) >= 7 * cus) return launch_tile<BF16, 192, 256, 2, 4, 2>(p, st);
-    if (2 * tiles(128, 256) >= cus) return launch_tile<BF16, 128, 256, 2, 4, 3>(p, st);
-    if (8 * tiles(128, 128) >= 5 * cus) return launch_tile<BF16, 128, 128, 2, 4, 4>(p, st);
+    const int64_t t256 = tiles(256, 256);
+    // tiles left after the last full round: in quarters where that is less
+    const int64_t rest = 37 * rounds(4 * (t256 % cus)) < 100 ? t256 % cus : 0;
+    const int64_t c256 =
+        direct(p) ? 100 * rounds(t256 - rest) + 37 * rounds(4 * rest) : INT64_MAX;
+    const int64_t c192 = 68 * rounds(tiles(192, 256)), c128 = 60 * rounds(tiles(128, 256));
+    const int64_t c_sq = 37 * rounds(tiles(128, 128)), least = std::min({c256, c192, c128, c_sq});
+    if (8 * tiles(128, 128) >= 5 * cus) {
+      if (c_sq == least) return launch_tile<BF16, 128, 128, 2, 4, 4>(p, st);
+      if (c128 == least) return launch_tile<BF16, 128, 256, 2, 4, 3>(p, st);
+      if (c192 == least) return launch_tile<BF16, 192, 256, 2, 4, 2>(p, st);
+      hipLaunchKernelGGL(fp8_quartered_kernel, dim3((unsigned)(t256 + 3 * rest)), dim3(256), 0, st,
+                         p, (uint32_t)(t256 - rest));
+      return;
+    }
   } else {
     if (tiles(128, 128) >= 2 * cus) return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
     if (tiles(128, 64) >= cus) return launch_tile<BF16, 128, 64, 2, 2, 2>(p, st);

@@ -122,6 +122,13 @@ def test_product_places(M, N, K):
         assert torch.equal(got, want.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("M,N,K", [(3600, 2060, 516), (3600, 2060, 390), (5000, 4616, 4612)])
+def test_product_places_many_tiles(M, N, K):
+    """The same where a bf16 output takes 192 x 256 tiles, in both ways of loading,
+    and 256 x 256 ones with the last of them in quarters."""
+    test_product_places(M, N, K)
+
+
 def test_product_nan_stays_in_its_row():
     import selective_state_space_52_amd as m
     for M in (20, 150):
