@@ -274,17 +274,6 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t t
   *tm = band * kBand + in - *tn * height;
 }
 
-// Asks for a half's LDS reads between its matrix instructions.
-template <class T, int kMore>
-__device__ __forceinline__ void interleave() {
-  constexpr int kReads = 2 * (T::kFm + T::kFn) + kMore, kMul = T::kFm * T::kFn;
-#pragma unroll
-  for (int i = 0; i < kMul; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMul - 1) / kMul, 0);
-  }
-}
-
 // DIRECT: rows start at multiples of 4 bytes, and buffer loads put 16 bytes a
 // lane straight into LDS, a wave 8 rows at a time in the order of the lanes
 // (the rotation of the pieces is in the lanes' addresses).  Rows past the
@@ -335,31 +324,29 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
   }
 
   i32x4 held[DIRECT ? 1 : T::kLoads];
-  auto load = [&](int kb, uint8_t* to) {
+  // load i of a step's, of the rows' block kb
+  auto load_one = [&](int kb, uint8_t* to, int i) {
+    const bool isa = i < T::kLoadsA;
     if constexpr (DIRECT) {
       // a piece past the last column, or with it inside: past the buffer's end
       const bool in = kb * kScaleBlock + spiece * 16 + 16 <= K;
       // (no step past K: the address is compared with the end less the step)
       const int step = min(kb * kScaleBlock, K);
-#pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) {
-        const bool isa = i < T::kLoadsA;
-        const int off = soff + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves) * K;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            isa ? ra : rb,
-            (__attribute__((address_space(3))) void*)(to + (i * T::kWaves + wave) * 1024), 16,
-            in ? off : 0x7FFFFFF0, step, 0, 0);
-      }
+      const int off = soff + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves) * K;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          isa ? ra : rb,
+          (__attribute__((address_space(3))) void*)(to + (i * T::kWaves + wave) * 1024), 16,
+          in ? off : 0x7FFFFFF0, step, 0, 0);
     } else {
-#pragma unroll
-      for (int i = 0; i < T::kLoads; ++i) {
-        const bool isa = i < T::kLoadsA;
-        // rows past the matrix: the last one again, whose results go nowhere
-        const int row = min(srow + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves),
-                            (isa ? rows_a : rows_b) - 1);
-        held[i] = load16_tail((isa ? ga : gb) + (int64_t)row * K, kb * kScaleBlock + spiece * 16, K);
-      }
+      // rows past the matrix: the last one again, whose results go nowhere
+      const int row = min(srow + (isa ? i : i - T::kLoadsA) * (8 * T::kWaves),
+                          (isa ? rows_a : rows_b) - 1);
+      held[i] = load16_tail((isa ? ga : gb) + (int64_t)row * K, kb * kScaleBlock + spiece * 16, K);
     }
+  };
+  auto load = [&](int kb, uint8_t* to) {
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) load_one(kb, to, i);
   };
   auto put = [&](uint8_t* to) {
     if constexpr (!DIRECT) {
@@ -428,54 +415,92 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
     Frag a[T::kFm], b[T::kFn];
   };
   const int arow = wm + (lane & 31), brow = BM + wn + (lane & 31);
-  auto read = [&](Half& f, const uint8_t* at, int h) {
-    const int c = 4 * h + 2 * (lane >> 5);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-      for (int i = 0; i < T::kFm; ++i)
-        f.a[i].h[q] = *reinterpret_cast<const i32x4*>(at + piece_at(arow + 32 * i, c + q));
-#pragma unroll
-      for (int j = 0; j < T::kFn; ++j)
-        f.b[j].h[q] = *reinterpret_cast<const i32x4*>(at + piece_at(brow + 32 * j, c + q));
-    }
+  constexpr int kFrags = T::kFm + T::kFn;
+  // read r of the 2 kFrags of a half
+  auto read = [&](Half& f, const uint8_t* at, int h, int r) {
+    const int q = r / kFrags, n = r % kFrags, c = 4 * h + 2 * (lane >> 5) + q;
+    const int row = n < T::kFm ? arow + 32 * n : brow + 32 * (n - T::kFm);
+    const i32x4 v = *reinterpret_cast<const i32x4*>(at + piece_at(row, c));
+    if (n < T::kFm) f.a[n % T::kFm].h[q] = v;
+    else f.b[(n - T::kFm) % T::kFn].h[q] = v;
   };
-  int sa[T::kFm], sb[T::kFn];
-  auto multiply = [&](const Half& f) {
-    if constexpr (BF16) {
+  using Scale = typename std::conditional<BF16, int, float>::type;
+  auto read_scales = [&](Scale (&ta)[T::kFm], Scale (&tb)[T::kFn], int k) {
+    const auto one = [&](int row) -> Scale {
+      const int code = scale[row * kScalePitch + k];
+      if constexpr (BF16) return code;
+      else return scale_value(code);
+    };
 #pragma unroll
-      for (int i = 0; i < T::kFm; ++i)
+    for (int i = 0; i < T::kFm; ++i) ta[i] = one(arow + 32 * i);
 #pragma unroll
-        for (int j = 0; j < T::kFn; ++j)
+    for (int j = 0; j < T::kFn; ++j) tb[j] = one(brow + 32 * j);
+  };
+  // For an fp32 output a quarter of a half's operands in bf16, and the next one.
+  bf16x8 wide[BF16 ? 1 : 2][kFrags];
+  auto widen = [&](const Half& f, int n, int q, const Scale (&ta)[T::kFm],
+                   const Scale (&tb)[T::kFn]) {
+    if constexpr (!BF16)
+      wide[q & 1][n] = n < T::kFm ? widen8(f.a[n % T::kFm], q, ta[n % T::kFm])
+                                  : widen8(f.b[(n - T::kFm) % T::kFn], q, tb[(n - T::kFm) % T::kFn]);
+  };
+  Scale sa[T::kFm], sb[T::kFn], next_sa[T::kFm], next_sb[T::kFn];
+  // The products of f; between them, where there is more, the reads of the half
+  // after it (half h of `at`, with scales na and nb) and, where `stage`, step kb's
+  // loads into `to`.  A load or a read that waits for its unit holds up what
+  // follows it in the wave, so they stand apart, one to a few for each matrix
+  // instruction (all of the loads first: 4096 x 4096 x 4096 61 us against 57, 8192 x
+  // 8192 x 8192 456 against 422).  Few matrix instructions in a step of which
+  // only the next is in flight leave no time for that: the loads come first (4096 x
+  // 2560 x 5120 in tiles of 192 x 256 by 8 waves: 54 us, apart 57).
+  auto multiply = [&](const Half& f, Half& next, const uint8_t* at, int h,
+                      const Scale (&na)[T::kFm], const Scale (&nb)[T::kFn], int kb, uint8_t* to,
+                      auto more, auto stage) {
+    constexpr bool kMore = decltype(more)::value, kStage = decltype(stage)::value;
+    constexpr int kMul = T::kFm * T::kFn, kQ = BF16 ? 1 : 4, kAll = kQ * kMul;
+    constexpr bool kReadsFirst = kMul == 1;
+    constexpr bool kLoadsFirst = !DIRECT || kMul == 1 || (S == 2 && kAll < 12);
+    constexpr int kSpan = (3 * kAll + 3) / 4, kEach = (2 * kFrags + kSpan - 1) / kSpan;
+    if constexpr (kStage && kLoadsFirst) load(kb, to);
+    if constexpr (kMore && kReadsFirst) {
+#pragma unroll
+      for (int r = 0; r < 2 * kFrags; ++r) read(next, at, h, r);
+    }
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+#pragma unroll
+      for (int m = 0; m < kMul; ++m) {
+        const int i = m / T::kFn, j = m % T::kFn, done = q * kMul + m;
+        if constexpr (BF16) {
           acc[i][j] = mfma32(f.b[j], f.a[i], acc[i][j], sb[j], sa[i]);
-    } else {
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              wide[q & 1][T::kFm + j], wide[q & 1][i], acc[i][j], 0, 0, 0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf16x8 aw[T::kFm], bw[T::kFn];
+          for (int n = m; n < kFrags; n += kMul) {
+            if (q < 3) widen(f, n, q + 1, sa, sb);
+            else if (kMore) widen(next, n, 0, na, nb);
+          }
+        }
+        if constexpr (kMore && !kReadsFirst) {
 #pragma unroll
-        for (int i = 0; i < T::kFm; ++i) aw[i] = widen8(f.a[i], q, scale_value(sa[i]));
+          for (int r = done * kEach; r < min(2 * kFrags, (done + 1) * kEach); ++r)
+            read(next, at, h, r);
+        }
+        if constexpr (kStage && !kLoadsFirst) {
 #pragma unroll
-        for (int j = 0; j < T::kFn; ++j) bw[j] = widen8(f.b[j], q, scale_value(sb[j]));
-#pragma unroll
-        for (int i = 0; i < T::kFm; ++i)
-#pragma unroll
-          for (int j = 0; j < T::kFn; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[j], aw[i], acc[i][j], 0, 0, 0);
+          for (int l = done * T::kLoads / kAll; l < (done + 1) * T::kLoads / kAll; ++l)
+            load_one(kb, to, l);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  };
-  auto read_scales = [&](int (&ta)[T::kFm], int (&tb)[T::kFn], int k) {
-#pragma unroll
-    for (int i = 0; i < T::kFm; ++i) ta[i] = scale[(arow + 32 * i) * kScalePitch + k];
-#pragma unroll
-    for (int j = 0; j < T::kFn; ++j) tb[j] = scale[(brow + 32 * j) * kScalePitch + k];
   };
 
   // Each half's operands are read while the half before it is multiplied.  In
   // the middle of a step, when its second half has been read by every wave,
   // its buffer takes the step S after it.
   Half f0, f1;
-  int next_sa[T::kFm], next_sb[T::kFn];
   for (int c0 = 0; c0 < kbs; c0 += T::kChunk) {
     const int n = min(T::kChunk, kbs - c0);
     const int due = ragged ? kbs - 1 - c0 : -1;  // the step that takes the rows' last bytes
@@ -492,15 +517,16 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
     __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 1) * T::kLoads : 0));
     if (due == 0) put_last(lds);
     __syncthreads();
-    read(f0, lds, 0);
+#pragma unroll
+    for (int r = 0; r < 2 * kFrags; ++r) read(f0, lds, 0, r);
     read_scales(sa, sb, 0);
+#pragma unroll
+    for (int n = 0; n < kFrags; ++n) widen(f0, n, 0, sa, sb);
     uint8_t* here = lds;
     for (int k = 0; k + 1 < n; ++k) {
       uint8_t* const there = here == lds + (S - 1) * kBuffer ? lds : here + kBuffer;
       __builtin_amdgcn_sched_barrier(0);
-      read(f1, here, 1);
-      multiply(f0);
-      interleave<T, 0>();
+      multiply(f0, f1, here, 1, sa, sb, 0, here, std::true_type(), std::false_type());
       __builtin_amdgcn_sched_barrier(0);
       // the next step's loads are done (a wave's loads into LDS count as its
       // vector memory, in order, and every step has kLoads of them), and this
@@ -514,11 +540,9 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
       __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 2) * T::kLoads : 0));
       barrier();
       __builtin_amdgcn_sched_barrier(0);
-      load(c0 + k + (DIRECT ? S : 2), here);
-      read(f0, there, 0);
       read_scales(next_sa, next_sb, k + 1);
-      multiply(f1);
-      interleave<T, T::kFm + T::kFn>();
+      multiply(f1, f0, there, 0, next_sa, next_sb, c0 + k + (DIRECT ? S : 2), here,
+               std::true_type(), std::true_type());
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < T::kFm; ++i) sa[i] = next_sa[i];
@@ -526,9 +550,8 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
       for (int j = 0; j < T::kFn; ++j) sb[j] = next_sb[j];
       here = there;
     }
-    read(f1, here, 1);
-    multiply(f0);
-    multiply(f1);
+    multiply(f0, f1, here, 1, sa, sb, 0, here, std::true_type(), std::false_type());
+    multiply(f1, f0, here, 0, sa, sb, 0, here, std::false_type(), std::false_type());
     // the loads past the last step still write to LDS
     __builtin_amdgcn_s_waitcnt(wait_loads(0));
     __syncthreads();
@@ -622,25 +645,26 @@ void launch_tile(const MatmulParams& p, hipStream_t st) {
     hipLaunchKernelGGL((fp8_tile_kernel<BF16, false, BM, BN, WM, WN, S>), grid, block, 0, st, p);
 }
 
-// The tile by the rounds in which the compute units work through them.  A full
-// round of 256 x 256 being 100, one of 192 x 256 takes 68, of 128 x 256 60, of 128 x
-// 128 37, quarters too (8192 x 10576 x 2560: 42, 29, 25 and 15 us).  Measured, us (M
+// The tile by the rounds in which the compute units work through them.  A round
+// of 256 x 256 being 100, one of 192 x 256 takes 70 to 79, of 128 x 256 60, of 128 x
+// 128 37, quarters too (8192 x 10576 x 2560: 41, 29, 25 and 15 us).  Measured, us (M
 // x N x K; in brackets what is taken):
 //                       256 in quarters  192 x 256  128 x 256  128 x 128  64 x 64
-//   8192 x  8192 x 8192     [446]           498
-//   8192 x 10576 x 2560     [222]           230        273        324        390
-//   4096 x 10576 x 2560      119           [111]
-//   4096 x  4096 x 4096      [58]            77
-//   4096 x  2560 x 5120       68            [51]
-//   2048 x  2560 x 5120                      49        [34]        46         50
-//   1024 x  2560 x 5120                      48         33        [23]        32
+//   8192 x  8192 x 8192     [422]           498        491        622
+//   8192 x 10576 x 2560     [220]           229        270        322        402
+//   8192 x  2560 x 5120     [101]           110        117        129
+//   4096 x 10576 x 2560     [125]           131        155
+//   4096 x  4096 x 4096      [57]            79         68         80        115
+//   4096 x  2560 x 5120       58            [53]        70         72         96
+//   2048 x  2560 x 5120       47             50        [34]        46         52
+//   1024 x  2560 x 5120       25             48         32        [23]        31
 //    128 x  2560 x 5120                      45         33         23        [14]
 // Through registers, rows of 256 x 256 tiles need more than there are (8192 x
 // 10576 x 2561: 885 us; 192 x 256: 652).
 // An fp32 output takes twice the matrix instructions and its operands'
-// widening, and stops at 128 x 128; with fewer than two of those for each CU,
-// 128 x 64 or 64 x 64 (3352 x 768 x 4096: 36, 33, 36; 8192 x 10576 x 2560:
-// 408, 483, 601).
+// widening, and stops at 128 x 128 (256 x 256: 398 us against 405 at 8192 x 10576 x
+// 2560).  Fewer tiles take 128 x 64 or 64 x 64 where one round is enough (us at K =
+// 4096; 3352 x 768: 33, 34, 38; 2560 x 768: 32, 23, 25; 1024 x 1024: 30, 22, 18).
 template <bool BF16>
 void launch(const MatmulParams& p, int cus, hipStream_t st) {
   const auto tiles = [&](int64_t bm, int64_t bn) {
@@ -665,7 +689,7 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
     const int64_t rest = 37 * rounds(4 * (t256 % cus)) < 100 ? t256 % cus : 0;
     const int64_t c256 =
         direct(p) ? 100 * rounds(t256 - rest) + 37 * rounds(4 * rest) : INT64_MAX;
-    const int64_t c192 = 68 * rounds(tiles(192, 256)), c128 = 60 * rounds(tiles(128, 256));
+    const int64_t c192 = 76 * rounds(tiles(192, 256)), c128 = 60 * rounds(tiles(128, 256));
     const int64_t c_sq = 37 * rounds(tiles(128, 128)), least = std::min({c256, c192, c128, c_sq});
     if (8 * tiles(128, 128) >= 5 * cus) {
       if (c_sq == least) return launch_tile<BF16, 128, 128, 2, 4, 4>(p, st);
@@ -675,9 +699,9 @@ void launch(const MatmulParams& p, int cus, hipStream_t st) {
                          p, (uint32_t)(t256 - rest));
       return;
     }
-  } else {
-    if (tiles(128, 128) >= 2 * cus) return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
-    if (tiles(128, 64) >= cus) return launch_tile<BF16, 128, 64, 2, 2, 2>(p, st);
+  } else if (tiles(64, 64) > cus) {
+    if (tiles(128, 64) <= cus) return launch_tile<BF16, 128, 64, 2, 2, 2>(p, st);
+    return launch_tile<BF16, 128, 128, 2, 2, 2>(p, st);
   }
   launch_tile<BF16, 64, 64, 2, 2, 4>(p, st);
 }

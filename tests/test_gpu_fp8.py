@@ -122,10 +122,12 @@ def test_product_places(M, N, K):
         assert torch.equal(got, want.to(torch.bfloat16))
 
 
-@pytest.mark.parametrize("M,N,K", [(3600, 2060, 516), (3600, 2060, 390), (5000, 4616, 4612)])
+@pytest.mark.parametrize("M,N,K", [(1100, 10500, 516), (1100, 10500, 390), (3600, 2060, 516), (3600, 2060, 390),
+                                   (4000, 4000, 516), (5000, 4616, 4612), (650, 700, 516)])
 def test_product_places_many_tiles(M, N, K):
     """The same where a bf16 output takes 192 x 256 tiles, in both ways of loading,
-    and 256 x 256 ones with the last of them in quarters."""
+    and 256 x 256 ones, whole and with the last of them in quarters; and an fp32
+    one 128 x 64."""
     test_product_places(M, N, K)
 
 
