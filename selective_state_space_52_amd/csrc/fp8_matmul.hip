@@ -32,6 +32,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(1)));  // at any address
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulParams p)
 // the bytes that a product moves through LDS cost clock as well as time.  A
 // wave's own tile decides those: 128 x 128 of a 256 x 256 one, by four waves,
 // reads a byte of LDS for 128 operations, 96 x 64 of a 192 x 256 one, by eight,
-// for 77: 2.48 against 2.20 PFLOP/s at 8192 x 8192 x 8192.  Of the rest, a tile's
+// for 77: 2.6 against 2.2 PFLOP/s at 8192 x 8192 x 8192.  Of the rest, a tile's
 // first loads and its stores take about 3 us.  The next step's loads issued
 // later in a step cost 7%.
 template <int BM, int BN, int WM, int WN, int S>
@@ -558,7 +559,9 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
   }
 
   // The tile goes out through LDS, 32 rows of a wave's tile at a time, so that
-  // a store covers whole lines of a row.
+  // a store covers whole lines of a row; past the caches, which hold what other
+  // tiles still read (8192 x 10576 x 2560 in bf16: 230 us without, 200 so; fp32:
+  // 410, 392).
   using Out = typename std::conditional<BF16, uint16_t, float>::type;
   constexpr int kWn = BN / WN, kPer = 16 / sizeof(Out);  // columns of a wave; of one store
   constexpr int kPitch = kWn * sizeof(Out) + 16;
@@ -590,7 +593,7 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
       Out* const to = out + row * p.N + c;
       if (row >= left_m || n <= 0) continue;
       if (n >= kPer) {
-        *reinterpret_cast<Any16*>(to) = Any16{{v.x, v.y, v.z, v.w}};
+        __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(to));
       } else {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -648,17 +651,17 @@ void launch_tile(const MatmulParams& p, hipStream_t st) {
 // The tile by the rounds in which the compute units work through them.  A round
 // of 256 x 256 being 100, one of 192 x 256 takes 70 to 79, of 128 x 256 60, of 128 x
 // 128 37, quarters too (8192 x 10576 x 2560: 41, 29, 25 and 15 us).  Measured, us (M
-// x N x K; in brackets what is taken):
+// x N x K; in brackets what is taken; the others with stores through the caches):
 //                       256 in quarters  192 x 256  128 x 256  128 x 128  64 x 64
-//   8192 x  8192 x 8192     [422]           498        491        622
-//   8192 x 10576 x 2560     [220]           229        270        322        402
-//   8192 x  2560 x 5120     [101]           110        117        129
-//   4096 x 10576 x 2560     [125]           131        155
-//   4096 x  4096 x 4096      [57]            79         68         80        115
+//   8192 x  8192 x 8192     [425]           498        491        622
+//   8192 x 10576 x 2560     [200]           229        270        322        402
+//   8192 x  2560 x 5120      [95]           110        117        129
+//   4096 x 10576 x 2560     [110]           131        155
+//   4096 x  4096 x 4096      [56]            79         68         80        115
 //   4096 x  2560 x 5120       58            [53]        70         72         96
-//   2048 x  2560 x 5120       47             50        [34]        46         52
-//   1024 x  2560 x 5120       25             48         32        [23]        31
-//    128 x  2560 x 5120                      45         33         23        [14]
+//   2048 x  2560 x 5120       47             50        [33]        46         52
+//   1024 x  2560 x 5120       25             48         32        [22]        31
+//    128 x  2560 x 5120                      45         33         23        [13]
 // Through registers, rows of 256 x 256 tiles need more than there are (8192 x
 // 10576 x 2561: 885 us; 192 x 256: 652).
 // An fp32 output takes twice the matrix instructions and its operands'
