@@ -232,8 +232,7 @@ __global__ void __launch_bounds__(64 * kFewWaves) fp8_few_kernel(MatmulParams p)
 // wave's own tile decides those: 128 x 128 of a 256 x 256 one, by four waves,
 // reads a byte of LDS for 128 operations, 96 x 64 of a 192 x 256 one, by eight,
 // for 77: 2.6 against 2.2 PFLOP/s at 8192 x 8192 x 8192.  Of the rest, a tile's
-// first loads and its stores take about 3 us.  The next step's loads issued
-// later in a step cost 7%.
+// first loads and its stores take about 3 us.
 template <int BM, int BN, int WM, int WN, int S>
 struct Tile {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
