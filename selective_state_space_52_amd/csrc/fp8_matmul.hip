@@ -515,7 +515,10 @@ __device__ __forceinline__ void tile_product(const MatmulParams& p, int64_t m0, 
     put(lds);
     if constexpr (!DIRECT) load(c0 + 1, lds);
     __builtin_amdgcn_s_waitcnt(wait_loads(DIRECT ? (S - 1) * T::kLoads : 0));
-    if (due == 0) put_last(lds);
+    if (due == 0) {  // after the zeros that every wave's loads put there
+      barrier();
+      put_last(lds);
+    }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < 2 * kFrags; ++r) read(f0, lds, 0, r);

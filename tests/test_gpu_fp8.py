@@ -131,6 +131,14 @@ def test_product_places_many_tiles(M, N, K):
     test_product_places(M, N, K)
 
 
+@pytest.mark.parametrize("M,N,K", [(200, 300, 4), (200, 300, 100), (200, 300, 124), (200, 300, 4108),
+                                   (3000, 4600, 100), (3000, 4600, 4108)])
+def test_product_places_last_bytes_first(M, N, K):
+    """The rows' last bytes, which fill no piece of 16, belong to the first step
+    of all or of a chunk of scales."""
+    test_product_places(M, N, K)
+
+
 def test_product_nan_stays_in_its_row():
     import selective_state_space_52_amd as m
     for M in (20, 150):
