@@ -573,7 +573,8 @@ typedef struct {
  * falling logit (equal ones by rising index):
  *   top_k keeps the first top_k; top_p keeps a token while the w before it sum
  *   to less than top_p times the sum of the first top_k; min_p keeps
- *   w >= min_p; the first token always stays.
+ *   w >= min_p; the first token always stays.  (top_p's sums are of w rounded to
+ *   2^-41: off by 1e-6 of the first token's at most, with 2^22 tokens.)
  * Of the kept tokens the one with the largest w / -log(noise) is taken (the
  * lowest index of equal ones).
  *   logits   : (rows, vocab) io dtype; -infinity and NaN are never taken

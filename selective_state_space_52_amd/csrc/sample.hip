@@ -34,7 +34,7 @@
 //
 // The vector instructions of the passes bound a batch of rows, latency a
 // single row.  Sums are in a fixed order or, where the order may differ, in
-// units of 2^-31 in 64-bit integers, so equal calls give equal tokens.
+// units of 2^-41 in 64-bit integers, so equal calls give equal tokens.
 #include "fp8.h"
 #include "mssm_internal.h"
 
@@ -47,7 +47,7 @@ constexpr int kFine = 512;   // of the distance below the largest logit
 constexpr int kList = 4096;  // tokens of the list in LDS
 constexpr int kRank = 256;   // ... that are ranked by comparing all pairs
 constexpr int kPer = kList / kThreads;
-constexpr float kUnits = 2147483648.0f;  // 2^31
+constexpr double kUnits = 2199023255552.0;  // 2^41: 2^22 tokens of w = 1 sum to 2^63
 
 // Unsigned order of floats: larger value, larger key.  Both zeros are equal.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -158,11 +158,15 @@ struct Weight {
     return x == max ? 0.0f : (x - max) * inv_t;
   }
   __device__ __forceinline__ float of(float x) const { return hw_exp2(scaled(x) * kLog2e); }
-  // w in units of 2^-31, rounded to the nearest: 50000 roundings of either sign
-  // are 6e-8 of the largest token's mass.  A NaN weight counts nothing.
+  // w in units of 2^-41, rounded to the nearest: V roundings, all of one sign
+  // where many logits are equal, are at most V 2^-42 of the largest token's mass
+  // (1e-6 for 2^22 tokens; in units of 2^-31 a tail of that many tokens could
+  // weigh 1e-3 and count nothing).  2^-41 is the last bit of a double from 2^11
+  // to 2^12, so adding 2^11 rounds to it.  A NaN weight counts nothing.
   __device__ __forceinline__ uint64_t units(float x) const { return units_of(of(x)); }
   static __device__ __forceinline__ uint64_t units_of(float v) {
-    return (uint32_t)__builtin_rintf(v * kUnits);
+    const double d = (double)fmaxf(v, 0.0f) + 2048.0;
+    return __builtin_bit_cast(uint64_t, d) & ((1ull << 52) - 1);
   }
   // The same without the look at the largest logit, which `scaled` needs where
   // that is infinite, or 1 / T nearly.
@@ -366,7 +370,7 @@ __device__ __forceinline__ void sample_by_digits(const SampleParams& p, const vo
   if (threadIdx.x == 0) {
     const int token = index_of(win);
     p.tokens[r] = token;
-    p.logprobs[r] = w.scaled(logit<BF16>(row, token)) - hw_log2((float)kept / kUnits) * kLn2;
+    p.logprobs[r] = w.scaled(logit<BF16>(row, token)) - hw_log2((float)((double)kept / kUnits)) * kLn2;
   }
 }
 
