@@ -541,6 +541,11 @@ typedef struct {
  *   a : (m, k) e4m3, a_scales (m, ceil(k / 128)) e8m0
  *   b : (n, k) e4m3, b_scales (ceil(n / b_block_rows), ceil(k / 128)) e8m0
  *   out : (m, n) out dtype, summed in fp32 and rounded once
+ * For an fp32 out the products are exact (a value of 2^128 or more counts as
+ * infinite).  For a bf16 one they are those of the 8-bit matrix instructions: of
+ * each 8 neighbouring k a product is cut, toward zero, at 2^-13 of the largest
+ * (1.5e-5 of a random sum, 2^-9 being the result's own rounding); a caller whose
+ * sums cancel to less than that asks for fp32.
  * A linear layer's three products: out = x w^T with b = w (128 x 128 blocks);
  * dx = dout w with a = dout in row blocks and b = w transposed; dw = dout^T x
  * with both quantised transposed and b_block_rows = 1.

@@ -217,8 +217,10 @@ def fp8_matmul(a, a_scales, b, b_scales, out_dtype=torch.bfloat16, out=None):
 
     a: (M, K), b: (N, K) float8_e4m3fn; a_scales: (M, ceil(K / 128)), b_scales:
     (ceil(N / 128), ceil(K / 128)) or (N, ceil(K / 128)), float8_e8m0fnu, as
-    quantize_fp8 and rms_norm_fwd_fp8 return them.  Summed in fp32; returns
-    (M, N) in out_dtype (bf16 or fp32).
+    quantize_fp8 and rms_norm_fwd_fp8 return them.  Returns (M, N) in out_dtype
+    (bf16 or fp32), or out.  Sums are fp32; the products are exact for an fp32
+    result, and for a bf16 one cut at 2^-13 of the largest of each 8 along k (see
+    mssm_fp8_matmul in include/mssm.h).
     """
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must have 2 dimensions")
