@@ -132,12 +132,18 @@ __device__ __forceinline__ void store4(void* out, int64_t at, int n, float a, fl
 //
 // A workgroup takes 16 rows of b and all of a's rows (MT tiles of 16); its 8
 // waves take every 8th block of 128, straight from memory into the
-// instruction's registers, up to kAhead blocks a turn, and their sums meet in
-// LDS.  b is read once; a's rows come from L2 to every workgroup, in as many
-// loads as b's, and the loads' addresses bound the kernel (16 x 10576 x 2560:
-// 10.1 us, 2.7 TB/s of b; 7.8 us for one row of a).  Holding all four blocks'
-// loads ahead of the first product costs the registers of half the waves: 14.1
-// us.
+// instruction's registers, and their sums meet in LDS.  b is read once; a's rows
+// come from L2 to every workgroup, in as many loads as b's.
+//
+// The memory's latency bounds it.  A turn has kAhead blocks, but which of them
+// there are depends on the wave, and the compiler moves each block's loads down
+// to its product: one block's loads (4 of 16 bytes and two scales; 6 and three with
+// 32 rows) are in flight a wave, and at K = 2560 a wave waits for memory up to
+// three times in a row.  45 registers (MT = 1) keep 8 waves a SIMD to cover that.
+// Holding all four blocks' loads ahead of the first product takes the registers of
+// half the waves: 14.1 us against 10.1.  N x K = 10576 x 2560, 10 calls in a graph:
+// 7.5 us for one row of a, 10.3 for 16 (2.6 TB/s of b), 14.0 for 32; fp32 outputs
+// 8.1, 10.6 and 14.6.
 constexpr int kFewWaves = 8;
 
 // WHOLE: rows of whole, aligned 16 bytes.
