@@ -54,8 +54,10 @@
  * Every launch of a call is on `stream`; the library creates no stream and
  * records no event of its own.
  *
- * Errors.  Every argument is validated before the first HIP call; a call that
- * fails validation returns a negative code and writes nothing.  A failing HIP
+ * Errors.  Every argument is validated before the first HIP call (the size of a
+ * workspace that depends on the device's compute units as soon as those are
+ * known); a call that fails validation returns a negative code, launches nothing
+ * and writes nothing.  A failing HIP
  * call returns MSSM_ERR_HIP; its message is kept per thread and returned by
  * mssm_last_error().  Non-finite inputs are not detected; they propagate
  * through the arithmetic.

@@ -171,6 +171,10 @@ int mssm_rms_norm_bwd(const void* dout, const void* r, const float* weight, cons
   const Range r_w = range(weight, dim * 4), r_rstd = range(rstd, rows * 4);
   const Range r_dres = range(dresidual, rows * dim * rs);
   if (aliased({r_dx, r_dr, r_dw}, {r_dout, r_r, r_w, r_rstd, r_dres})) return MSSM_ERR_ALIAS;
+  // one that is missing or misaligned, whatever the size
+  rc = mssm::check_workspace(workspace, workspace_bytes, 1);
+  if (rc != MSSM_OK) return rc;
+  // the first HIP call: the size goes by the device's compute units
   const int cus = mssm::compute_units();
   const int64_t need = mssm::rms_norm_bwd_workspace(rows, (int)dim, cus);
   rc = mssm::check_workspace(workspace, workspace_bytes, need);
