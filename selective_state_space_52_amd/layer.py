@@ -266,7 +266,7 @@ def sample_tokens(logits, noise, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
             _is(v, name, dtype, (rows,), dev)
             setattr(args, name + "_row", v.data_ptr())
         elif name == "top_k":
-            args.top_k = min(int(v), 2**31 - 1)
+            args.top_k = max(0, min(int(v), 2**31 - 1))     # ctypes would cut it to 32 bits
         else:
             setattr(args, name, v)
     tokens = torch.empty(rows, dtype=torch.int64, device=dev)
