@@ -665,7 +665,8 @@ void launch_tile(const MatmulParams& p, hipStream_t st) {
 // The tile by the rounds in which the compute units work through them.  A round
 // of 256 x 256 being 100, one of 192 x 256 takes 70 to 79, of 128 x 256 60, of 128 x
 // 128 37, quarters too (8192 x 10576 x 2560: 41, 29, 25 and 15 us).  Measured, us (M
-// x N x K; in brackets what is taken; the others with stores through the caches):
+// x N x K; in brackets what is taken; the others with stores through the caches; 20
+// calls in a row, single ones after a pause take up to a seventh more):
 //                       256 in quarters  192 x 256  128 x 256  128 x 128  64 x 64
 //   8192 x  8192 x 8192     [425]           498        491        622
 //   8192 x 10576 x 2560     [200]           229        270        322        402
@@ -677,7 +678,7 @@ void launch_tile(const MatmulParams& p, hipStream_t st) {
 //   1024 x  2560 x 5120       25             48         32        [22]        31
 //    128 x  2560 x 5120                      45         33         23        [13]
 // Through registers, rows of 256 x 256 tiles need more than there are (8192 x
-// 10576 x 2561: 885 us; 192 x 256: 652).
+// 10576 x 2561: 885 us; 192 x 256: 652, 6 registers of which are spilled).
 // An fp32 output takes twice the matrix instructions and its operands'
 // widening, and stops at 128 x 128 (256 x 256: 398 us against 405 at 8192 x 10576 x
 // 2560).  Fewer tiles take 128 x 64 or 64 x 64 where one round is enough (us at K =
