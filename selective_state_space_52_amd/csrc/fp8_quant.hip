@@ -7,9 +7,9 @@
 // The division is by a power of two, so each value is rounded once.  An
 // infinity becomes NaN; it and NaN leave the block's scale alone.  The
 // kernels read and write each value once: HBM bounds large ones along rows (4096 x
-// 3352 bf16: 8.6 us, 4.8 TB/s).  A workgroup of the others loads, waits and stores
-// its 128 rows once: 12 us transposed (15 with the workgroups in row order), 12.4 for
-// 128 x 128 blocks, 9.8 for those transposed, 3.4 to 4.2 TB/s.
+// 3352 bf16: 8.7 us, 4.7 TB/s).  A workgroup of the others loads, waits and stores
+// its 128 rows once: 12 us transposed (15 with the workgroups in row order), 12.7 for
+// 128 x 128 blocks, 9.8 for those transposed, 3.2 to 4.2 TB/s.
 #include "fp8.h"
 #include "mssm_internal.h"
 
