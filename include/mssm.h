@@ -637,6 +637,188 @@ int mssm_mamba2_state_update(float* state, void* conv_state, const void* xbc, co
 int mssm_mamba2_state_update_workspace(const mssm_step_dims* dims, int64_t* bytes);
 
 /*
+ * ---- The ends of a training step.
+ *
+ * The embedding's rows and their gradient, the log-probabilities of given
+ * tokens and the losses on them, and the optimiser's step.  Memory, streams,
+ * workspaces and errors are as for the layer's operators; sums are taken in a
+ * fixed order, so equal calls give equal bits.
+ */
+typedef struct {
+  int64_t rows;         /* tokens, 1 to 2^31 - 1                              */
+  int64_t vocab;        /* rows of the table, 1 to 2^22                       */
+  int64_t dim;          /* columns, 1 to 2^20                                 */
+  int64_t io_stride;    /* elements from one row of out (dout) to the next;   */
+                        /* 0 = dim                                            */
+  int32_t table_dtype;  /* mssm_dtype of table (dtable)                       */
+  int32_t io_dtype;     /* mssm_dtype of out (dout)                           */
+  float scale;
+  int32_t add;          /* backward: nonzero adds to what dtable holds        */
+} mssm_embed_dims;
+
+/*
+ * out[i] = scale * table[tokens[i]], in fp32 and rounded once.  A token outside
+ * [0, vocab) is padding (the -1 of mssm_sample, say): its row is zero.
+ *   tokens : (rows) int64;  table : (vocab, dim);  out : (rows, dim)
+ */
+int mssm_embedding_fwd(const int64_t* tokens, const void* table, void* out,
+                       const mssm_embed_dims* dims, void* stream);
+
+/*
+ * The table's gradient: dtable[v] = scale * (sum of dout[i] over the i with
+ * tokens[i] = v), in fp32 and rounded once.  Without `add` all of dtable is
+ * written (zeros where no token names a row); with it the sums are added to
+ * what it holds (the gradient of an output projection that shares the table,
+ * say), and rows that no token names are not touched.  Padding gives nothing,
+ * whatever its dout holds.
+ */
+int mssm_embedding_bwd(const int64_t* tokens, const void* dout, void* dtable, void* workspace,
+                       int64_t workspace_bytes, const mssm_embed_dims* dims, void* stream);
+int mssm_embedding_bwd_workspace(const mssm_embed_dims* dims, int64_t* bytes);
+
+typedef struct {
+  int64_t rows;           /* 1 to 2^22 - 1                                    */
+  int64_t vocab;          /* 1 to 2^22                                        */
+  int64_t logits_stride;  /* elements from one row to the next; 0 = vocab     */
+  int64_t grad_stride;    /* the same of dlogits                              */
+  int32_t io_dtype;       /* mssm_dtype of logits and dlogits                 */
+  float temperature;      /* > 0, finite                                      */
+} mssm_logprob_dims;
+
+/*
+ * Log-probabilities of given tokens: with z = logits / temperature,
+ *     logprobs[i] = z[i, tokens[i]] - log(sum_j exp(z[i, j]))
+ * in fp32.  A token outside [0, vocab) marks a row without one (a prompt's, say):
+ * its log-probability is 0 and its logits are not read.  A logit of -infinity
+ * has probability zero; a NaN, an infinity or nothing but -infinity in a row
+ * makes that row NaN.
+ *   logits : (rows, vocab) io dtype;  tokens : (rows) int64
+ *   logprobs : (rows) fp32
+ *   stats  : (rows, 2) fp32, what the backward call needs: the row's largest logit
+ *            and log(sum_j exp((logits - largest) / temperature)); or NULL
+ */
+int mssm_token_logprobs_fwd(const void* logits, const int64_t* tokens, float* logprobs,
+                            float* stats, const mssm_logprob_dims* dims, void* stream);
+
+/*
+ * Its gradient for dlogprobs (rows) fp32:
+ *     dlogits[i, j] = dlogprobs[i] / temperature * ([j = tokens[i]] - p[i, j])
+ * with p the softmax of z.  Rows without a token, and those whose dlogprobs is
+ * 0, are zero, and their logits are not read.  dlogits may be `logits` itself
+ * (of the same stride), which it then replaces.
+ */
+int mssm_token_logprobs_bwd(const void* logits, const int64_t* tokens, const float* stats,
+                            const float* dlogprobs, void* dlogits, const mssm_logprob_dims* dims,
+                            void* stream);
+
+typedef struct {
+  mssm_logprob_dims dims;
+  float clip_low;   /* ratios are clipped to [1 - clip_low, 1 + clip_high]; */
+  float clip_high;  /* both >= 0                                            */
+  float kl_coef;    /* >= 0                                                 */
+  int32_t reserved;
+} mssm_policy_args;
+
+/*
+ * Clipped policy loss with a KL term and its gradient, from one read of the
+ * logits.  Per row, with logp as mssm_token_logprobs_fwd gives it:
+ *     ratio = exp(logp - old_logprobs)
+ *     loss  = -min(ratio A, clip(ratio) A) + kl_coef (exp(x) - 1 - x),
+ *     x = ref_logprobs - logp                 (an estimate of KL(policy || ref))
+ *     dlogits = weights d(loss)/d(logits)
+ * so dlogits is the gradient of sum_i weights[i] loss[i]; where both sides of
+ * the min are equal its slope is the unclipped one's.  A row without a token has
+ * loss and logp 0 and a zero gradient, whatever its other entries hold; one
+ * whose loss has no slope (clipped, no KL term) or whose weight is 0 a zero
+ * gradient.
+ *   old_logprobs, advantages : (rows) fp32
+ *   ref_logprobs : (rows) fp32, or NULL (no KL term)
+ *   weights      : (rows) fp32, or NULL (1)
+ *   loss, logprobs : (rows) fp32, unweighted
+ *   dlogits      : (rows, vocab) io dtype, or NULL (not computed); it may be
+ *                  `logits` itself (of the same stride)
+ */
+int mssm_policy_loss(const void* logits, const int64_t* tokens, const float* old_logprobs,
+                     const float* advantages, const float* ref_logprobs, const float* weights,
+                     float* loss, float* logprobs, void* dlogits, const mssm_policy_args* args,
+                     void* stream);
+
+typedef struct {
+  int64_t rows;           /* 1 to 2^31 - 1                                    */
+  int64_t pairs;          /* 1 to 2^20                                        */
+  float beta;             /* finite                                           */
+  float label_smoothing;  /* 0 to 1                                           */
+} mssm_preference_args;
+
+/*
+ * Preference loss of pairs of sequences packed in rows, and its gradient.
+ * Sequence s has rows offsets[s] to offsets[s + 1] - 1; pair p is sequence 2p
+ * (preferred) and 2p + 1 (rejected).  With S(s) = sum over a sequence's rows of
+ * logprobs - ref_logprobs (in 64 bits) and d = beta (S(2p) - S(2p + 1)):
+ *     loss[p] = -(1 - e) log sigmoid(d) - e log sigmoid(-d),  e = label_smoothing
+ *     dlogprobs = weights[p] d(loss[p])/d(logprobs)
+ * Rows of no sequence (before the first, behind the last) get 0.
+ *   logprobs, ref_logprobs : (rows) fp32 (0 in both for a prompt's rows)
+ *   offsets   : (2 pairs + 1) int32, not falling, within [0, rows]; a sequence
+ *               may be empty.  Values outside count as the nearest inside.
+ *   weights   : (pairs) fp32, or NULL (1)
+ *   loss      : (pairs) fp32, unweighted;  dlogprobs : (rows) fp32
+ */
+int mssm_preference_loss(const float* logprobs, const float* ref_logprobs, const int32_t* offsets,
+                         const float* weights, float* loss, float* dlogprobs,
+                         const mssm_preference_args* args, void* stream);
+
+typedef struct {
+  float* param;        /* updated in place                                   */
+  const void* grad;
+  void* copy;          /* bf16, receives the new param; or NULL              */
+  int64_t size;        /* elements, 1 to 2^35                                */
+  float weight_decay;
+  int32_t grad_dtype;  /* mssm_dtype                                         */
+} mssm_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;  /* betas in [0, 1), eps >= 0                 */
+  double grad_scale;             /* gradients are multiplied by it            */
+  int64_t step;                  /* 1, 2, ...                                 */
+  uint64_t seed;                 /* of the 8-bit states' rounding             */
+  int32_t state_bits;            /* 32 or 8                                   */
+  int32_t reserved;
+  /* one value each, on the device, in place of the numbers above; each may be
+   * NULL.  (A captured graph reads them anew in every replay.) */
+  const float* lr_value;
+  const float* grad_scale_value;
+  const int64_t* step_value;
+} mssm_adamw_args;
+
+/*
+ * AdamW step of `count` tensors.  Per element, with g = grad_scale * grad:
+ *     m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *     param = param (1 - lr weight_decay)
+ *             - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * The tensors' states lie one after another in m and v, each tensor's from a
+ * multiple of 128 elements on (so m has sum of ceil(size / 128) * 128 elements);
+ * what lies between is zero and stays zero.  All are cleared before the first
+ * step.
+ *   state_bits 32: m, v fp32; m_scales and v_scales NULL
+ *   state_bits 8 : m, v e4m3 and an fp32 scale for each 128 of them in m_scales,
+ *     v_scales: m = value * scale, sqrt(v) = value * scale.  A block's scale is
+ *     its largest value / 448 (0 where that is below 2^-100).  Moments change by
+ *     a small part of themselves in a step, which rounding to nearest would
+ *     undo; so a value x goes to one of its two e4m3 neighbours at the odds
+ *     that keep its mean: to floor(x / unit + u) unit.  u is element i's
+ *     fraction, the upper 24 bits of w + i k (mod 2^32); k = 0x9E3779B9 and w
+ *     the lower half of h for m, k = 0x6A09E667 and the upper half for v;
+ *     h = y xor (y >> 32) (all mod 2^64) of y = (t xor (t >> 32)) *
+ *     0x6A09E667F3BCC909, t = (seed + step) * 0x9E3779B97F4A7C15.  No nonzero
+ *     sqrt(v) goes to zero.  The step itself uses the unrounded moments.
+ * NaN and infinities stay in their element (as NaN in 8 bits).
+ * The list of tensors is read during the call.  Up to 64 tensors take one launch.
+ */
+int mssm_adamw(const mssm_adamw_tensor* tensors, int64_t count, void* m, void* v, float* m_scales,
+               float* v_scales, const mssm_adamw_args* args, void* stream);
+
+/*
  * Issue-rate probe of the vector ALU, for the roofline of the scan, which is
  * bound by its exponentials and fp32 multiply-adds rather than by HBM
  * (page "What are State Space Models (SSMs)?", Key Features: the selective

@@ -25,8 +25,12 @@ from ._lib import (MSSM_BF16, MSSM_F32, MSSM_FLAG_BC_STATE_MAJOR, MSSM_FLAG_LAYO
 
 from .layer import (fp8_matmul, mamba2_state_update, quantize_fp8, rms_norm_bwd, rms_norm_fwd,
                     rms_norm_fwd_fp8, sample_tokens)
+from .train import (adamw_state, adamw_step, embedding_bwd, embedding_fwd, policy_loss,
+                    preference_loss, token_logprobs_bwd, token_logprobs_fwd)
 
-__all__ = ["rms_norm_fwd", "rms_norm_fwd_fp8", "rms_norm_bwd", "quantize_fp8", "fp8_matmul",
+__all__ = ["embedding_fwd", "embedding_bwd", "token_logprobs_fwd", "token_logprobs_bwd",
+           "policy_loss", "preference_loss", "adamw_state", "adamw_step",
+           "rms_norm_fwd", "rms_norm_fwd_fp8", "rms_norm_bwd", "quantize_fp8", "fp8_matmul",
            "sample_tokens", "mamba2_state_update", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_fwd_conv",
            "causal_conv1d_fwd", "selective_state_update", "mamba2_scan_fwd", "scan_plan",
            "workspace_size", "set_scan_timing_events", "MssmError", "abi_version"]

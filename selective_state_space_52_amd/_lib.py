@@ -38,7 +38,10 @@ EXPORTS = ("mssm_selective_scan_fwd", "mssm_selective_scan_bwd",
            "mssm_rms_norm_fwd", "mssm_rms_norm_fwd_fp8", "mssm_rms_norm_bwd",
            "mssm_rms_norm_bwd_workspace", "mssm_quantize_fp8", "mssm_fp8_matmul",
            "mssm_sample", "mssm_mamba2_state_update",
-           "mssm_mamba2_state_update_workspace")
+           "mssm_mamba2_state_update_workspace",
+           "mssm_embedding_fwd", "mssm_embedding_bwd", "mssm_embedding_bwd_workspace",
+           "mssm_token_logprobs_fwd", "mssm_token_logprobs_bwd", "mssm_policy_loss",
+           "mssm_preference_loss", "mssm_adamw")
 
 
 class Dims(ctypes.Structure):
@@ -96,6 +99,44 @@ class StepDims(ctypes.Structure):
                 ("xbc_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
                 ("z_stride", ctypes.c_int64), ("width", ctypes.c_int32),
                 ("io_dtype", ctypes.c_int32)]
+
+
+class EmbedDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("io_stride", ctypes.c_int64), ("table_dtype", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("add", ctypes.c_int32)]
+
+
+class LogprobDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("logits_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
+                ("io_dtype", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
+class PolicyArgs(ctypes.Structure):
+    _fields_ = [("dims", LogprobDims), ("clip_low", ctypes.c_float),
+                ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class PreferenceArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("pairs", ctypes.c_int64), ("beta", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("size", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamwArgs(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("lr_value", ctypes.c_void_p), ("grad_scale_value", ctypes.c_void_p),
+                ("step_value", ctypes.c_void_p)]
 
 
 _lib = None
@@ -186,6 +227,16 @@ def lib():
         sig("mssm_sample", [vp] * 4 + [ctypes.POINTER(SampleArgs), vp])
         sig("mssm_mamba2_state_update", [vp] * 10 + [i] + [vp] * 3 + [i64, sd, vp])
         sig("mssm_mamba2_state_update_workspace", [sd, out64])
+        ed, ld = ctypes.POINTER(EmbedDims), ctypes.POINTER(LogprobDims)
+        sig("mssm_embedding_fwd", [vp] * 3 + [ed, vp])
+        sig("mssm_embedding_bwd", [vp] * 4 + [i64, ed, vp])
+        sig("mssm_embedding_bwd_workspace", [ed, out64])
+        sig("mssm_token_logprobs_fwd", [vp] * 4 + [ld, vp])
+        sig("mssm_token_logprobs_bwd", [vp] * 5 + [ld, vp])
+        sig("mssm_policy_loss", [vp] * 9 + [ctypes.POINTER(PolicyArgs), vp])
+        sig("mssm_preference_loss", [vp] * 6 + [ctypes.POINTER(PreferenceArgs), vp])
+        sig("mssm_adamw", [ctypes.POINTER(AdamwTensor), i64] + [vp] * 4
+            + [ctypes.POINTER(AdamwArgs), vp])
         _lib = L
     return _lib
 

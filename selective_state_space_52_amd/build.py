@@ -24,7 +24,8 @@ SOURCES = ["scan_fwd.hip", "scan_fwd_n1_8.hip", "scan_fwd_n16.hip",
            "scan_bwd.hip", "state_update.hip", "conv1d.hip", "mamba2.hip",
            "noalloc.hip", "probe.hip", "mssm_api.cpp",
            "rms_norm.hip", "fp8_quant.hip", "fp8_matmul.hip", "sample.hip",
-           "mamba2_step.hip", "layer_api.cpp"]
+           "mamba2_step.hip", "layer_api.cpp",
+           "embedding.hip", "token_loss.hip", "adamw.hip", "train_api.cpp"]
 
 # Packed fp32 VALU forms are switched off for every device compilation.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

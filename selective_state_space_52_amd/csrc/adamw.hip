@@ -1,0 +1,173 @@
+// adamw.hip -- the AdamW step of many tensors in one launch, states in fp32 or
+// in 8 bits.
+//
+//   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// The 8-bit states are e4m3 values of m and sqrt(v), not v: the root halves the
+// range in powers of two, and e4m3 with a block's scale spans 2^18 below the
+// block's largest.  Each block of 128 has an fp32 scale, its largest value /
+// 448, so that a block whose values all fall by a thousandth does so in its
+// scale.  A value goes to one of its two neighbours by a fraction u that has
+// each value's mean kept (rounding to nearest would never let a moment move by
+// less than half a unit, 3% to 6% of it, in a step).  u walks through the
+// elements as a sequence of equal steps modulo 1 (2^32 / golden ratio, and 2^32
+// times the root of 2's fraction for the second state), shifted by a hash of
+// the seed and the step; for one element it is spread evenly over the steps.
+#include "fp8.h"
+#include "mssm_internal.h"
+
+namespace mssm {
+namespace {
+
+constexpr int kThreads = 256, kUnroll = 2;
+constexpr int kStrip = kThreads * 8;          // elements of one pass, 8 a thread
+constexpr int kElements = kStrip * kUnroll;   // of a workgroup
+constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f;
+constexpr uint32_t kStrideM = 0x9E3779B9u, kStrideV = 0x6A09E667u;
+
+struct Rates {
+  float lr, grad_scale, inv_c1, inv_c2;
+  uint32_t shift_m, shift_v;
+};
+__device__ __forceinline__ Rates rates_of(const AdamParams& p) {
+  Rates r;
+  r.lr = p.lr_value ? *p.lr_value : p.lr;
+  r.grad_scale = p.grad_scale_value ? *p.grad_scale_value : p.grad_scale;
+  r.inv_c1 = p.inv_c1;
+  r.inv_c2 = p.inv_c2;
+  int64_t step = p.step;
+  if (p.step_value) {
+    step = *p.step_value;
+    // 1 - b^t; expm1 keeps its digits where b^t is close to 1
+    r.inv_c1 = 1.0f / -expm1f((float)step * p.log_beta1);
+    r.inv_c2 = 1.0f / sqrtf(-expm1f((float)step * p.log_beta2));
+  }
+  uint64_t x = (p.seed + (uint64_t)step) * 0x9E3779B97F4A7C15ull;
+  x = (x ^ x >> 32) * 0x6A09E667F3BCC909ull;
+  x ^= x >> 32;
+  r.shift_m = (uint32_t)x;
+  r.shift_v = (uint32_t)(x >> 32);
+  return r;
+}
+
+__device__ __forceinline__ void load8_fp8(float (&v)[8], const void* p, int64_t i) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
+  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false);
+  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+  v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+}
+
+// x, of the block that 16 neighbouring lanes hold, as e4m3 at p + i.
+template <bool POSITIVE>
+__device__ __forceinline__ void store8_rounded(void* p, float* scales, int64_t i, float (&x)[8],
+                                               uint32_t u, uint32_t stride) {
+  float most = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = finite_or_nan(x[j]);
+    most = fmaxf(most, fabsf(x[j]));
+  }
+  most = max16(most);
+  if (most < kSmallest) most = 0.0f;
+  const float up = most > 0.0f ? kMost8 / most : 0.0f;
+  if ((threadIdx.x & 15) == 0) scales[i / kScaleBlock] = most / kMost8;
+  float q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float y = x[j] * up, a = fabsf(y);
+    // the value's unit: 3 mantissa bits below its power of two, at least 2^-9
+    const uint32_t e = max(__float_as_uint(a) >> 23, 121u);
+    const float unit = __uint_as_float((e - 3) << 23), per = __uint_as_float((257 - e) << 23);
+    const float dither = (float)((u + j * stride) >> 8) * 0x1p-24f;
+    float size = fminf(floorf(__fadd_rn(a * per, dither)) * unit, kMost8);
+    if (POSITIVE && x[j] > 0.0f && most > 0.0f) size = fmaxf(size, 0x1p-9f);
+    q[j] = a == a ? copysignf(size, y) : y;
+  }
+  const uint2 w = {pack_fp8x4(q[0], q[1], q[2], q[3]), pack_fp8x4(q[4], q[5], q[6], q[7])};
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = w;
+}
+
+template <bool EIGHT>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
+  // the tensor whose workgroup this is: the last that begins at or before it
+  const int lane = threadIdx.x & 63;
+  const uint32_t first = lane < p.count ? p.first[lane] : 0xFFFFFFFFu;
+  const int which = __popcll(__ballot(first <= blockIdx.x)) - 1;
+  const AdamTensor& t = p.tensors[which];
+  const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * kElements;
+  const Rates r = rates_of(p);
+  const float keep = 1.0f - r.lr * t.decay;
+#pragma unroll
+  for (int c = 0; c < kUnroll; ++c) {
+    const int64_t i = begin + c * kStrip + threadIdx.x * 8;
+    const int64_t left = t.size - i;
+    // the states go on to the end of the last block of 128
+    if (begin + c * kStrip + (int64_t)(threadIdx.x & ~15) * 8 >= t.size) continue;
+    const int n = (int)min((int64_t)8, left);
+    float w[8], g[8], m[8], v[8];
+    if (n > 0) {
+      load8<false>(w, t.param, i, n);
+      if (t.grad_bf16)
+        load8<true>(g, t.grad, i, n);
+      else
+        load8<false>(g, t.grad, i, n);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = g[j] = 0.0f;
+    }
+    const int64_t at = t.at + i;
+    if constexpr (EIGHT) {
+      load8_fp8(m, p.m, at);
+      load8_fp8(v, p.v, at);
+      const float ms = p.m_scales[at / kScaleBlock], vs = p.v_scales[at / kScaleBlock];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] *= ms;
+        v[j] *= vs;
+        v[j] *= v[j];
+      }
+    } else {
+      load8<false>(m, p.m, at, 8);
+      load8<false>(v, p.v, at, 8);
+    }
+    float root[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // each product rounded by itself, as the definition reads
+      const float s = __fmul_rn(g[j], r.grad_scale);
+      m[j] = __fadd_rn(__fmul_rn(m[j], p.beta1), __fmul_rn(s, p.rest1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], p.beta2), __fmul_rn(__fmul_rn(s, s), p.rest2));
+      root[j] = sqrtf(v[j]);
+      const float update = m[j] * r.inv_c1 * hw_rcp(root[j] * r.inv_c2 + p.eps);
+      w[j] = w[j] * keep - r.lr * update;
+    }
+    if (n > 0) {
+      store8<false>(t.param, i, n, w);
+      if (t.copy) store8<true>(t.copy, i, n, w);
+    }
+    if constexpr (EIGHT) {
+      store8_rounded<false>(p.m, p.m_scales, at, m, r.shift_m + (uint32_t)i * kStrideM, kStrideM);
+      store8_rounded<true>(p.v, p.v_scales, at, root, r.shift_v + (uint32_t)i * kStrideV, kStrideV);
+    } else {
+      store8<false>(p.m, at, 8, m);
+      store8<false>(p.v, at, 8, v);
+    }
+  }
+}
+
+}  // namespace
+
+int64_t adamw_block_elements() { return kElements; }
+
+hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st) {
+  auto kernel = eight ? adamw_kernel<true> : adamw_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3(p.blocks), dim3(kThreads), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace mssm

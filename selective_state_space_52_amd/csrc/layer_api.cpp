@@ -1,62 +1,13 @@
 // layer_api.cpp -- the C ABI of the layer's operators around the scans
 // (declared in include/mssm.h): argument validation, always before the first
 // HIP call, and dispatch on the caller's stream.
-#include <hip/hip_runtime.h>
-
 #include <cstring>
-#include <initializer_list>
 
-#include "mssm.h"
-#include "mssm_internal.h"
+#include "api_checks.h"
+
+using namespace mssm::api;
 
 namespace {
-
-constexpr int64_t kMost = INT64_MAX / 16;  // elements of one array
-constexpr int64_t kGrid = INT32_MAX;       // workgroups of one launch
-constexpr int64_t kItems = UINT32_MAX;     // threads of one launch
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-int64_t blocks128(int64_t n) { return (n + 127) / 128; }
-int64_t size_of(int32_t dtype) { return dtype == MSSM_BF16 ? 2 : 4; }
-bool known(int32_t dtype) { return dtype == MSSM_F32 || dtype == MSSM_BF16; }
-
-// a * b <= limit for positive a, b.
-bool fits(int64_t a, int64_t b, int64_t limit = kMost) { return a > 0 && b > 0 && a <= limit / b; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void* p, int64_t bytes) {
-  return p && bytes > 0 ? Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes} : Range{0, 0};
-}
-// Rows of `cols` elements, `stride` apart.
-Range rows_range(const void* p, int64_t rows, int64_t cols, int64_t stride, int64_t size) {
-  return range(p, ((rows - 1) * stride + cols) * size);
-}
-bool overlap(Range a, Range b) {
-  return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-// Whether an output overlaps an input or another output.
-bool aliased(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Range& i : ins)
-      if (overlap(*o, i)) return true;
-    for (const Range* q = o + 1; q != outs.end(); ++q)
-      if (overlap(*o, *q)) return true;
-  }
-  return false;
-}
-bool all_aligned(std::initializer_list<const void*> ps, size_t a) {
-  for (const void* p : ps)
-    if (p && !aligned(p, a)) return false;
-  return true;
-}
-
-int done(hipError_t e, const char* what) {
-  if (e == hipSuccess) return MSSM_OK;
-  mssm::set_hip_error(what, e);
-  return MSSM_ERR_HIP;
-}
 
 int check_norm_dims(const mssm_norm_dims* d) {
   if (!d) return MSSM_ERR_NULL;

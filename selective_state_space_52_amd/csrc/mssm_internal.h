@@ -376,4 +376,95 @@ struct Mamba2StepParams {
 };
 hipError_t launch_mamba2_step(const Mamba2StepParams& p, bool bf16, int cus, hipStream_t st);
 
+// ---- the ends of a training step (train_api.cpp)
+
+struct EmbedParams {
+  const int64_t* tokens;
+  const void* table;      // forward
+  void* out;
+  int64_t rows, io_stride;
+  int32_t vocab, dim;
+  float scale;
+};
+hipError_t launch_embedding(const EmbedParams& p, bool table_bf16, bool io_bf16, hipStream_t st);
+
+struct EmbedBwdParams {
+  const int64_t* tokens;
+  const void* dout;
+  void* dtable;
+  void* workspace;
+  int64_t rows, io_stride;
+  int32_t vocab, dim;
+  float scale;
+  int32_t add;
+};
+int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t dim);
+hipError_t launch_embedding_bwd(const EmbedBwdParams& p, bool table_bf16, bool io_bf16,
+                                hipStream_t st);
+
+// Log-probabilities, with old_logprobs the policy loss.  Null pointers: not
+// wanted.
+struct LogprobParams {
+  const void* logits;
+  const int64_t* tokens;
+  float* logprobs;
+  float* stats;               // (rows, 2)
+  const float* old_logprobs;
+  const float* advantages;
+  const float* ref_logprobs;
+  const float* weights;
+  float* loss;
+  const float* dlogprobs;     // backward
+  void* dlogits;
+  int64_t rows, logits_stride, grad_stride;
+  int32_t vocab;
+  float inv_temperature, clip_lo, clip_hi, kl_coef;
+};
+hipError_t launch_logprobs(const LogprobParams& p, bool bf16, hipStream_t st);
+hipError_t launch_logprobs_bwd(const LogprobParams& p, bool bf16, hipStream_t st);
+
+struct PreferenceParams {
+  const float* logprobs;
+  const float* ref_logprobs;
+  const int32_t* offsets;
+  const float* weights;       // may be null
+  float* loss;
+  float* dlogprobs;
+  int32_t rows, pairs;
+  float beta, smoothing;
+};
+hipError_t launch_preference(const PreferenceParams& p, hipStream_t st);
+
+// One launch of the optimiser: up to kAdamTensors tensors.
+constexpr int kAdamTensors = 64;
+struct AdamTensor {
+  float* param;
+  const void* grad;
+  void* copy;
+  int64_t size, at;           // at: the first element of its states
+  float decay;
+  int32_t grad_bf16;
+};
+struct AdamParams {
+  AdamTensor tensors[kAdamTensors];
+  uint32_t first[kAdamTensors];  // each tensor's first workgroup
+  void* m;
+  void* v;
+  float* m_scales;
+  float* v_scales;
+  const float* lr_value;
+  const float* grad_scale_value;
+  const int64_t* step_value;
+  uint64_t seed;
+  int64_t step;
+  float lr, grad_scale, eps;
+  float beta1, beta2, rest1, rest2;  // rest = 1 - beta
+  float log_beta1, log_beta2;
+  float inv_c1, inv_c2;       // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  int32_t count;
+  uint32_t blocks;
+};
+int64_t adamw_block_elements();
+hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st);
+
 }  // namespace mssm
