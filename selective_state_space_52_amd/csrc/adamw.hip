@@ -20,11 +20,67 @@
 namespace mssm {
 namespace {
 
-constexpr int kThreads = 256, kUnroll = 2;
-constexpr int kStrip = kThreads * 8;          // elements of one pass, 8 a thread
+// 4 elements a thread in each of 4 passes, so that a wave's accesses are of whole
+// neighbouring lines (1 KB of fp32); 32 lanes hold a block.
+constexpr int kThreads = 256, kPer = 4, kUnroll = 4;
+constexpr int kStrip = kThreads * kPer;       // elements of one pass
 constexpr int kElements = kStrip * kUnroll;   // of a workgroup
+constexpr int kBlockLanes = kScaleBlock / kPer;
 constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f;
 constexpr uint32_t kStrideM = 0x9E3779B9u, kStrideV = 0x6A09E667u;
+
+// v[0..3] = p[i..i+3], the values past `n` >= 1 of them zero.
+template <bool BF16>
+__device__ __forceinline__ void load4(float (&v)[4], const void* p, int64_t i, int n) {
+  if constexpr (BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    uint32_t a, b;
+    if (n >= 4) {
+      const Any8 w = *reinterpret_cast<const Any8*>(q);
+      a = w.w[0], b = w.w[1];
+    } else {
+      a = q[0] | (n > 1 ? (uint32_t)q[1] << 16 : 0u);
+      b = n > 2 ? q[2] : 0u;
+    }
+    v[0] = bf16_lo(a), v[1] = bf16_hi(a), v[2] = bf16_lo(b), v[3] = bf16_hi(b);
+  } else {
+    const float* q = static_cast<const float*>(p) + i;
+    if (n >= 4) {
+      const Any16 w = *reinterpret_cast<const Any16*>(q);
+      v[0] = __uint_as_float(w.w[0]), v[1] = __uint_as_float(w.w[1]);
+      v[2] = __uint_as_float(w.w[2]), v[3] = __uint_as_float(w.w[3]);
+    } else {
+      v[0] = q[0], v[1] = n > 1 ? q[1] : 0.0f, v[2] = n > 2 ? q[2] : 0.0f, v[3] = 0.0f;
+    }
+  }
+}
+// Past the caches: a step's data are more than they hold, and not read again soon.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+template <bool BF16>
+__device__ __forceinline__ void store4(void* p, int64_t i, int n, const float (&v)[4]) {
+  if constexpr (BF16) {
+    uint16_t* q = static_cast<uint16_t*>(p) + i;
+    if (n >= 4) {
+      const u32x2_any w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x2_any*>(q));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) q[j] = to_bf16(v[j]);
+    }
+  } else {
+    float* q = static_cast<float*>(p) + i;
+    if (n >= 4) {
+      const u32x4_any w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                           __float_as_uint(v[3])};
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(q));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) q[j] = v[j];
+    }
+  }
+}
 
 struct Rates {
   float lr, grad_scale, inv_c1, inv_c2;
@@ -51,34 +107,32 @@ __device__ __forceinline__ Rates rates_of(const AdamParams& p) {
   return r;
 }
 
-__device__ __forceinline__ void load8_fp8(float (&v)[8], const void* p, int64_t i) {
+__device__ __forceinline__ void load4_fp8(float (&v)[4], const void* p, int64_t i) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + i);
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false);
-  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
-  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false);
-  const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+  const int w = *reinterpret_cast<const int*>(static_cast<const uint8_t*>(p) + i);
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-  v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
-// x, of the block that 16 neighbouring lanes hold, as e4m3 at p + i.
+// x, of the block that 32 neighbouring lanes hold, as e4m3 at p + i.
 template <bool POSITIVE>
-__device__ __forceinline__ void store8_rounded(void* p, float* scales, int64_t i, float (&x)[8],
+__device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i, float (&x)[4],
                                                uint32_t u, uint32_t stride) {
   float most = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < kPer; ++j) {
     x[j] = finite_or_nan(x[j]);
     most = fmaxf(most, fabsf(x[j]));
   }
   most = max16(most);
+  most = fmaxf(most, __shfl_xor(most, 16));
   if (most < kSmallest) most = 0.0f;
   const float up = most > 0.0f ? kMost8 / most : 0.0f;
-  if ((threadIdx.x & 15) == 0) scales[i / kScaleBlock] = most / kMost8;
-  float q[8];
+  if ((threadIdx.x & (kBlockLanes - 1)) == 0) scales[i / kScaleBlock] = most / kMost8;
+  float q[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < kPer; ++j) {
     const float y = x[j] * up, a = fabsf(y);
     // the value's unit: 3 mantissa bits below its power of two, at least 2^-9
     const uint32_t e = max(__float_as_uint(a) >> 23, 121u);
@@ -88,8 +142,8 @@ __device__ __forceinline__ void store8_rounded(void* p, float* scales, int64_t i
     if (POSITIVE && x[j] > 0.0f && most > 0.0f) size = fmaxf(size, 0x1p-9f);
     q[j] = a == a ? copysignf(size, y) : y;
   }
-  const uint2 w = {pack_fp8x4(q[0], q[1], q[2], q[3]), pack_fp8x4(q[4], q[5], q[6], q[7])};
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + i) = w;
+  __builtin_nontemporal_store(pack_fp8x4(q[0], q[1], q[2], q[3]),
+                              reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i));
 }
 
 template <bool EIGHT>
@@ -104,40 +158,40 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
   const float keep = 1.0f - r.lr * t.decay;
 #pragma unroll
   for (int c = 0; c < kUnroll; ++c) {
-    const int64_t i = begin + c * kStrip + threadIdx.x * 8;
+    const int64_t i = begin + c * kStrip + threadIdx.x * kPer;
     const int64_t left = t.size - i;
     // the states go on to the end of the last block of 128
-    if (begin + c * kStrip + (int64_t)(threadIdx.x & ~15) * 8 >= t.size) continue;
-    const int n = (int)min((int64_t)8, left);
-    float w[8], g[8], m[8], v[8];
+    if (begin + c * kStrip + (int64_t)(threadIdx.x & ~(kBlockLanes - 1)) * kPer >= t.size) continue;
+    const int n = (int)min((int64_t)kPer, left);
+    float w[4], g[4], m[4], v[4];
     if (n > 0) {
-      load8<false>(w, t.param, i, n);
+      load4<false>(w, t.param, i, n);
       if (t.grad_bf16)
-        load8<true>(g, t.grad, i, n);
+        load4<true>(g, t.grad, i, n);
       else
-        load8<false>(g, t.grad, i, n);
+        load4<false>(g, t.grad, i, n);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = g[j] = 0.0f;
+      for (int j = 0; j < kPer; ++j) w[j] = g[j] = 0.0f;
     }
     const int64_t at = t.at + i;
     if constexpr (EIGHT) {
-      load8_fp8(m, p.m, at);
-      load8_fp8(v, p.v, at);
+      load4_fp8(m, p.m, at);
+      load4_fp8(v, p.v, at);
       const float ms = p.m_scales[at / kScaleBlock], vs = p.v_scales[at / kScaleBlock];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kPer; ++j) {
         m[j] *= ms;
         v[j] *= vs;
         v[j] *= v[j];
       }
     } else {
-      load8<false>(m, p.m, at, 8);
-      load8<false>(v, p.v, at, 8);
+      load4<false>(m, p.m, at, 4);
+      load4<false>(v, p.v, at, 4);
     }
-    float root[8];
+    float root[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kPer; ++j) {
       // each product rounded by itself, as the definition reads
       const float s = __fmul_rn(g[j], r.grad_scale);
       m[j] = __fadd_rn(__fmul_rn(m[j], p.beta1), __fmul_rn(s, p.rest1));
@@ -147,15 +201,15 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
       w[j] = w[j] * keep - r.lr * update;
     }
     if (n > 0) {
-      store8<false>(t.param, i, n, w);
-      if (t.copy) store8<true>(t.copy, i, n, w);
+      store4<false>(t.param, i, n, w);
+      if (t.copy) store4<true>(t.copy, i, n, w);
     }
     if constexpr (EIGHT) {
-      store8_rounded<false>(p.m, p.m_scales, at, m, r.shift_m + (uint32_t)i * kStrideM, kStrideM);
-      store8_rounded<true>(p.v, p.v_scales, at, root, r.shift_v + (uint32_t)i * kStrideV, kStrideV);
+      store4_rounded<false>(p.m, p.m_scales, at, m, r.shift_m + (uint32_t)i * kStrideM, kStrideM);
+      store4_rounded<true>(p.v, p.v_scales, at, root, r.shift_v + (uint32_t)i * kStrideV, kStrideV);
     } else {
-      store8<false>(p.m, at, 8, m);
-      store8<false>(p.v, at, 8, v);
+      store4<false>(p.m, at, 4, m);
+      store4<false>(p.v, at, 4, v);
     }
   }
 }

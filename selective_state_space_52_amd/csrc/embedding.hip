@@ -4,6 +4,8 @@
 //   dtable[v] = scale * sum of dout[i] over the i with tokens[i] = v  (+ dtable[v])
 //
 // A token outside the table is padding: a zero row, and no gradient.
+#include <type_traits>
+
 #include "fp8.h"
 #include "mssm_internal.h"
 
@@ -58,11 +60,23 @@ SortPlan sort_plan(int64_t vocab) {
   return SortPlan{(int)((vocab + range - 1) / range), (int)range};
 }
 
-template <bool TBF>
+// A wave's tokens from i on, 64 apart, as loads that are in flight together; -1
+// past the end.
+constexpr int kBatch = 8;
+__device__ __forceinline__ void load_tokens(int64_t (&t)[kBatch], const int64_t* tokens, int64_t i,
+                                            int64_t end) {
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int64_t at = i + b * 64;
+    t[b] = tokens[at < end ? at : end - 1];
+    if (at >= end) t[b] = -1;
+  }
+}
+
 __global__ void __launch_bounds__(kSortThreads)
     embedding_sort_kernel(const int64_t* __restrict__ tokens, int rows, int vocab, int range,
                           int* __restrict__ order, int* __restrict__ named, int* __restrict__ count,
-                          void* __restrict__ dtable, int dim) {
+                          uint8_t* __restrict__ present) {
   extern __shared__ uint32_t cursor[];  // [kSortWaves][range]
   __shared__ uint32_t part[kSortWaves], below_part[kSortWaves];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -75,11 +89,15 @@ __global__ void __launch_bounds__(kSortThreads)
   const int64_t begin = min((int64_t)rows, (int64_t)wave * run);
   const int64_t end = min((int64_t)rows, begin + run);
   uint32_t below = 0;
-  for (int64_t i = begin + lane; i < end; i += 64) {
-    const int64_t t = tokens[i];
-    if (t >= 0 && t < first) ++below;
-    const int64_t at = t - first;
-    if (at >= 0 && at < mine) atomicAdd(&cursor[wave * range + (int)at], 1u);
+  for (int64_t i = begin; i < end; i += 64 * kBatch) {
+    int64_t t[kBatch];
+    load_tokens(t, tokens, i + lane, end);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (t[b] >= 0 && t[b] < first) ++below;
+      const int64_t at = t[b] - first;
+      if (at >= 0 && at < mine) atomicAdd(&cursor[wave * range + (int)at], 1u);
+    }
   }
   for (int d = 32; d > 0; d >>= 1) below += __shfl_xor(below, d);
   if (lane == 0) below_part[wave] = below;
@@ -109,38 +127,32 @@ __global__ void __launch_bounds__(kSortThreads)
       at += c;
     }
   if (blockIdx.x == gridDim.x - 1 && v == mine - 1) *count = (int)at;
-  // rows that no token names are cleared here
-  __shared__ uint32_t empty[kSortRange / 32];
-  const uint64_t none = __ballot(v < mine && total == 0);
-  if (lane == 0) empty[wave * 2] = (uint32_t)none, empty[wave * 2 + 1] = (uint32_t)(none >> 32);
+  if (present && v < mine) present[first + v] = total != 0;
   __syncthreads();
-  for (int64_t i = begin; i < end; i += 64) {
-    const int64_t t = i + lane < end ? tokens[i + lane] : -1;
-    const int64_t own = t - first;
-    const bool in = own >= 0 && own < mine;
-    uint64_t left = __ballot(in);
-    while (left) {  // one different token of the 64 a turn
-      const int leader = __ffsll((unsigned long long)left) - 1;
-      const int token = __builtin_amdgcn_readlane((int)own, leader);
-      const uint64_t same = __ballot(in && (int)own == token);
-      uint32_t place = 0;
-      if (lane == leader)
-        place = atomicAdd(&cursor[wave * range + token], (uint32_t)__popcll(same));
-      place = __builtin_amdgcn_readlane((int)place, leader);
-      if (same >> lane & 1) {
-        const uint32_t to = place + (uint32_t)__popcll(same & ((1ull << lane) - 1));
-        order[to] = (int)(i + lane);
-        named[to] = first + token;
+  for (int64_t i = begin; i < end; i += 64 * kBatch) {
+    int64_t t[kBatch];
+    load_tokens(t, tokens, i + lane, end);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t own = t[b] - first;
+      const bool in = own >= 0 && own < mine;
+      uint64_t left = __ballot(in);
+      while (left) {  // one different token of the 64 a turn
+        const int leader = __ffsll((unsigned long long)left) - 1;
+        const int token = __builtin_amdgcn_readlane((int)own, leader);
+        const uint64_t same = __ballot(in && (int)own == token);
+        uint32_t place = 0;
+        if (lane == leader)
+          place = atomicAdd(&cursor[wave * range + token], (uint32_t)__popcll(same));
+        place = __builtin_amdgcn_readlane((int)place, leader);
+        if (same >> lane & 1) {
+          const uint32_t to = place + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+          order[to] = (int)(i + b * 64 + lane);
+          named[to] = first + token;
+        }
+        left &= ~same;
       }
-      left &= ~same;
     }
-  }
-  if (dtable == nullptr) return;
-  for (int r = wave; r < mine; r += kSortWaves) {
-    if (!(empty[r >> 5] >> (r & 31) & 1)) continue;
-    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int64_t to = (int64_t)(first + r) * dim;
-    for (int i = lane * 8; i < dim; i += 512) store8<TBF>(dtable, to + i, dim - i, zero);
   }
 }
 
@@ -149,9 +161,12 @@ struct Pieces {
   const int* order;
   const int* named;
   const int* count;
+  const uint8_t* present;
   float* head;   // (pieces, dim): the sum of the token that came in from the piece before
   float* tail;   // (pieces, dim): of the one that goes on into the next
   int len, slices;
+  int sums;      // workgroups that sum; those after them clear
+  U32Div chunks; // 16 bytes each, of a row of the gradient
 };
 
 template <bool TBF>
@@ -169,36 +184,95 @@ __device__ __forceinline__ void finish(const EmbedBwdParams& p, int token, int c
   store8<TBF>(p.dtable, to, n, sum);
 }
 
+// Clears the rows that no token names, in pieces of 16 bytes: kClear a thread.
+constexpr int kClear = 16;
+template <bool TBF>
+__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, const Pieces& q, int64_t block) {
+  constexpr int kCols = TBF ? 8 : 4;
+  typedef typename std::conditional<TBF, uint16_t, uint32_t>::type T;
+  const int chunks = (p.dim + kCols - 1) / kCols;
+  const int64_t first = block * (kThreads * kClear);
+  const int64_t row0 = first / chunks;
+  const uint32_t at0 = (uint32_t)(first - row0 * chunks) + threadIdx.x;
+#pragma unroll 4
+  for (int c = 0; c < kClear; ++c) {
+    const uint32_t at = at0 + c * kThreads, down = udiv(at, q.chunks);
+    const int64_t row = row0 + down;
+    if (row >= p.vocab) return;
+    const int col = (int)(at - down * chunks) * kCols, n = p.dim - col;
+    if (q.present[row]) continue;
+    T* to = static_cast<T*>(p.dtable) + row * p.dim + col;
+    if (n >= kCols) {
+      *reinterpret_cast<Any16*>(to) = Any16{{0, 0, 0, 0}};
+    } else {
+      for (int j = 0; j < n; ++j) to[j] = 0;
+    }
+  }
+}
+
+// One wave a piece and slice of columns.  Its lanes hold the piece's rows and
+// tokens; 8 rows' loads are in flight together.
 template <bool TBF, bool OBF>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams p, Pieces q) {
+  if ((int)blockIdx.x >= q.sums) {
+    clear_rows<TBF>(p, q, (int)blockIdx.x - q.sums);
+    return;
+  }
   const int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
   const int64_t piece = item / q.slices;
-  const int col = (int)(item % q.slices) * 512 + (threadIdx.x & 63) * 8;
-  const int count = *q.count;
-  const int64_t begin = piece * q.len, end = min((int64_t)count, begin + q.len);
-  if (begin >= count || col >= p.dim) return;
+  const int lane = threadIdx.x & 63;
+  const int col = (int)(item % q.slices) * 512 + lane * 8;
+  const int count = __builtin_amdgcn_readfirstlane(*q.count);
+  const int64_t begin = piece * q.len;
+  if (begin >= count) return;
+  const int len = (int)min((int64_t)q.len, count - begin);
+  const int held = min(lane, len - 1);
+  const int rows = q.order[begin + held], names = q.named[begin + held];
+  bool came_in = begin > 0 && q.named[begin - 1] == __builtin_amdgcn_readfirstlane(names);
+  const bool goes_on =
+      begin + len < count && q.named[begin + len] == __builtin_amdgcn_readlane(names, len - 1);
   const int n = p.dim - col;
-  bool came_in = begin > 0 && q.named[begin - 1] == q.named[begin];
-  const bool goes_on = end < count && q.named[end] == q.named[end - 1];
+  const bool whole = n >= 8;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  int token = q.named[begin];
-  for (int64_t i = begin; i < end; ++i) {
-    const int next = q.named[i];
-    if (next != token) {
-      if (came_in)
-        store8<false>(q.head, piece * p.dim + col, n, sum);
-      else
-        finish<TBF>(p, token, col, sum);
-      came_in = false;
-      token = next;
+  int token = __builtin_amdgcn_readfirstlane(names);
+  constexpr int kRows = 8;
+  for (int i = 0; i < len; i += kRows) {
+    Raw8<OBF> raw[kRows];
+    if (whole) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+      for (int r = 0; r < kRows; ++r) {
+        const int64_t row = __builtin_amdgcn_readlane(rows, min(i + r, len - 1));
+        raw[r] = load_raw8<OBF>(p.dout, row * p.io_stride + col);
+      }
     }
-    float v[8];
-    load8<OBF>(v, p.dout, (int64_t)q.order[i] * p.io_stride + col, n);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    for (int r = 0; r < kRows; ++r) {
+      if (i + r >= len) break;
+      const int next = __builtin_amdgcn_readlane(names, i + r);
+      if (next != token) {
+        if (n > 0) {
+          if (came_in)
+            store8<false>(q.head, piece * p.dim + col, n, sum);
+          else
+            finish<TBF>(p, token, col, sum);
+        }
+        came_in = false;
+        token = next;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+      }
+      float v[8];
+      if (whole)
+        unpack8<OBF>(v, raw[r]);
+      else if (n > 0)
+        load8<OBF>(v, p.dout, (int64_t)__builtin_amdgcn_readlane(rows, i + r) * p.io_stride + col, n);
+      else
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
   }
+  if (n <= 0) return;
   if (came_in)
     store8<false>(q.head, piece * p.dim + col, n, sum);
   else if (goes_on)
@@ -207,32 +281,79 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams 
     finish<TBF>(p, token, col, sum);
 }
 
-// The piece in which a token across pieces begins adds up its sums, in order.
+// The piece in which a token across pieces begins adds up its sums: a workgroup
+// for it and a slice of columns, whose waves take runs of the pieces, 8 loads in
+// flight, and are added in order.
+constexpr int kJoinWaves = kThreads / 64;
 template <bool TBF>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams p, Pieces q) {
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
-  const int64_t piece = item / q.slices;
-  const int col = (int)(item % q.slices) * 512 + (threadIdx.x & 63) * 8;
+  __shared__ float part[kJoinWaves][64][9];
+  const int64_t piece = blockIdx.x / q.slices;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int col = (int)(blockIdx.x % q.slices) * 512 + lane * 8;
   const int count = *q.count;
   const int64_t begin = piece * q.len, end = begin + q.len;
-  if (end >= count || col >= p.dim) return;
+  if (end >= count) return;
   const int token = q.named[end];
-  if (q.named[end - 1] != token) return;                    // nothing goes on
-  if (begin > 0 && q.named[begin - 1] == token) return;     // it began earlier
-  const int n = p.dim - col;
-  float sum[8];
-  load8<false>(sum, q.tail, piece * p.dim + col, n);
-  for (int64_t at = end; at < count && q.named[at] == token; at += q.len) {
-    float v[8];
-    load8<false>(v, q.head, at / q.len * p.dim + col, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+  if (q.named[end - 1] != token) return;                 // nothing goes on
+  if (begin > 0 && q.named[begin - 1] == token) return;  // it began earlier
+  // the pieces that it reaches: 64 of their first places a turn
+  int64_t pieces = 0;
+  for (;;) {
+    const int64_t at = end + (pieces + lane) * q.len;
+    const uint64_t in = __ballot(at < count && q.named[at < count ? at : 0] == token);
+    if (in != ~0ull) {
+      pieces += __builtin_ctzll(~in);
+      break;
+    }
+    pieces += 64;
   }
+  const int n = p.dim - col;
+  const int64_t each = (pieces + kJoinWaves - 1) / kJoinWaves;
+  const int64_t from = wave * each, to = min(pieces, from + each);
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n > 0) {
+    if (wave == 0) load8<false>(sum, q.tail, piece * p.dim + col, n);
+    const int64_t at = (piece + 1) * p.dim + col;
+    int64_t i = from;
+    for (; i + 8 <= to; i += 8) {
+      float v[8][8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) load8<false>(v[r], q.head, at + (i + r) * p.dim, n);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
+    }
+    for (; i < to; ++i) {
+      float v[8];
+      load8<false>(v, q.head, at + i * p.dim, n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[wave][lane][j] = sum[j];
+  __syncthreads();
+  if (wave != 0 || n <= 0) return;
+  for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += part[w][lane][j];
   finish<TBF>(p, token, col, sum);
 }
 
-constexpr int kLen = 32;
-int64_t pieces_of(int64_t rows) { return (rows + kLen - 1) / kLen; }
+// Places of a piece: 8 at least, 64 (its wave's lanes) at most, in between as
+// many as give 2048 waves.
+int len_of(int64_t rows, int64_t dim) {
+  const int64_t waves = rows * ((dim + 511) / 512);
+  int len = 8;
+  while (len < 64 && waves / len > 2048) len *= 2;
+  return len;
+}
+int64_t pieces_of(int64_t rows, int64_t dim) {
+  const int len = len_of(rows, dim);
+  return (rows + len - 1) / len;
+}
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
@@ -249,8 +370,8 @@ hipError_t launch_embedding(const EmbedParams& p, bool table_bf16, bool io_bf16,
 }
 
 int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t dim) {
-  (void)vocab;
-  return 256 + 2 * round256(rows * 4) + 2 * round256(pieces_of(rows) * dim * 4);
+  return 256 + 2 * round256(rows * 4) + round256(vocab) +
+         2 * round256(pieces_of(rows, dim) * dim * 4);
 }
 
 hipError_t launch_embedding_bwd(const EmbedBwdParams& p, bool table_bf16, bool io_bf16,
@@ -263,29 +384,33 @@ hipError_t launch_embedding_bwd(const EmbedBwdParams& p, bool table_bf16, bool i
   ws += round256(p.rows * 4);
   int* named = reinterpret_cast<int*>(ws);
   ws += round256(p.rows * 4);
-  const int64_t pieces = pieces_of(p.rows);
+  uint8_t* present = p.add ? nullptr : reinterpret_cast<uint8_t*>(ws);
+  ws += round256(p.vocab);
+  const int64_t pieces = pieces_of(p.rows, p.dim);
   q.head = reinterpret_cast<float*>(ws);
   q.tail = reinterpret_cast<float*>(ws + round256(pieces * p.dim * 4));
-  q.order = order; q.named = named; q.count = count;
-  q.len = kLen;
+  q.order = order; q.named = named; q.count = count; q.present = present;
+  q.len = len_of(p.rows, p.dim);
   q.slices = (p.dim + 511) / 512;
+  const int64_t chunks = table_bf16 ? (p.dim + 7) / 8 : (p.dim + 3) / 4;
+  q.chunks = make_u32div((uint32_t)chunks);
   const SortPlan s = sort_plan(p.vocab);
   const size_t lds = (size_t)kSortWaves * s.range * 4;
-  auto sort = table_bf16 ? embedding_sort_kernel<true> : embedding_sort_kernel<false>;
-  hipLaunchKernelGGL(sort, dim3((unsigned)s.groups), dim3(kSortThreads), lds, st, p.tokens,
-                     (int)p.rows, p.vocab, s.range, order, named, count,
-                     p.add ? nullptr : p.dtable, p.dim);
+  hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)s.groups), dim3(kSortThreads), lds, st,
+                     p.tokens, (int)p.rows, p.vocab, s.range, order, named, count, present);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t per = kThreads / 64;
-  const dim3 grid((unsigned)((pieces * q.slices + per - 1) / per));
+  q.sums = (int)((pieces * q.slices + per - 1) / per);
+  const int64_t clears = p.add ? 0 : (p.vocab * chunks + kThreads * kClear - 1) / (kThreads * kClear);
+  const dim3 grid((unsigned)(q.sums + clears));
   auto sum = table_bf16 ? (io_bf16 ? embedding_sum_kernel<true, true> : embedding_sum_kernel<true, false>)
                         : (io_bf16 ? embedding_sum_kernel<false, true> : embedding_sum_kernel<false, false>);
   hipLaunchKernelGGL(sum, grid, dim3(kThreads), 0, st, p, q);
   e = hipGetLastError();
-  if (e != hipSuccess || pieces == 1) return e;
+  if (e != hipSuccess || pieces == 1) return e;  // one piece: nothing goes on
   auto join = table_bf16 ? embedding_join_kernel<true> : embedding_join_kernel<false>;
-  hipLaunchKernelGGL(join, grid, dim3(kThreads), 0, st, p, q);
+  hipLaunchKernelGGL(join, dim3((unsigned)((pieces - 1) * q.slices)), dim3(kThreads), 0, st, p, q);
   return hipGetLastError();
 }
 

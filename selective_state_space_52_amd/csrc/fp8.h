@@ -79,6 +79,29 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* p, int64_t i, i
   }
 }
 
+// 8 elements as they lie in memory, for loads that are to be in flight together.
+template <bool BF16>
+struct Raw8 {
+  Any16 a[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> load_raw8(const void* p, int64_t i) {
+  return *reinterpret_cast<const Raw8<BF16>*>(static_cast<const char*>(p) + i * (BF16 ? 2 : 4));
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack8(float (&v)[8], const Raw8<BF16>& r) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo(r.a[0].w[j]);
+      v[2 * j + 1] = bf16_hi(r.a[0].w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.a[j >> 2].w[j & 3]);
+  }
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (BF16) {
@@ -109,6 +132,27 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&
       for (int j = 0; j < 8; ++j)
         if (j < n) q[j] = v[j];
     }
+  }
+}
+
+// The same past the caches, for results too many to be found there again.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+template <bool BF16>
+__device__ __forceinline__ void store8_past(void* p, int64_t i, int n, const float (&v)[8]) {
+  if (n < 8) {
+    store8<BF16>(p, i, n, v);
+  } else if constexpr (BF16) {
+    const u32x4_any a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(a, reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i));
+  } else {
+    u32x4_any* q = reinterpret_cast<u32x4_any*>(static_cast<float*>(p) + i);
+    const u32x4_any a = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                         __float_as_uint(v[3])};
+    const u32x4_any b = {__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                         __float_as_uint(v[7])};
+    __builtin_nontemporal_store(a, q);
+    __builtin_nontemporal_store(b, q + 1);
   }
 }
 

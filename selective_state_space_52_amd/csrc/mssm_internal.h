@@ -419,9 +419,10 @@ struct LogprobParams {
   int64_t rows, logits_stride, grad_stride;
   int32_t vocab;
   float inv_temperature, clip_lo, clip_hi, kl_coef;
+  int32_t past;               // the gradient is stored past the caches; set by the launch
 };
-hipError_t launch_logprobs(const LogprobParams& p, bool bf16, hipStream_t st);
-hipError_t launch_logprobs_bwd(const LogprobParams& p, bool bf16, hipStream_t st);
+hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st);
+hipError_t launch_logprobs_bwd(LogprobParams p, bool bf16, hipStream_t st);
 
 struct PreferenceParams {
   const float* logprobs;

@@ -21,8 +21,11 @@ int check_embed_dims(const mssm_embed_dims* d) {
     return MSSM_ERR_DIMS;
   if (d->io_stride != 0 && (d->io_stride < d->dim || !fits(d->rows, d->io_stride)))
     return MSSM_ERR_DIMS;
-  // at most one wave for each 512 columns of a row, in both directions
-  if (!fits(d->rows, (d->dim + 511) / 512 * 64, kItems)) return MSSM_ERR_DIMS;
+  // at most one wave for each 512 columns of a row, in both directions, and in
+  // the backward a thread for 64 columns of the table
+  if (!fits(d->rows, (d->dim + 511) / 512 * 64, kItems / 2) ||
+      !fits(d->vocab, (d->dim + 3) / 4, kItems / 2 * 16 - 4096))
+    return MSSM_ERR_DIMS;
   return MSSM_OK;
 }
 
