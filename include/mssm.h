@@ -674,6 +674,7 @@ int mssm_embedding_fwd(const int64_t* tokens, const void* table, void* out,
  */
 int mssm_embedding_bwd(const int64_t* tokens, const void* dout, void* dtable, void* workspace,
                        int64_t workspace_bytes, const mssm_embed_dims* dims, void* stream);
+/* 0 (then NULL may be given) for up to 1024 rows. */
 int mssm_embedding_bwd_workspace(const mssm_embed_dims* dims, int64_t* bytes);
 
 typedef struct {
@@ -698,7 +699,11 @@ typedef struct {
  *            and log(sum_j exp((logits - largest) / temperature)); or NULL
  */
 int mssm_token_logprobs_fwd(const void* logits, const int64_t* tokens, float* logprobs,
-                            float* stats, const mssm_logprob_dims* dims, void* stream);
+                            float* stats, void* workspace, int64_t workspace_bytes,
+                            const mssm_logprob_dims* dims, void* stream);
+/* Workspace of this call and of mssm_policy_loss: 0 (then NULL may be given) up
+ * to a vocabulary of 65536, else parts of a row are summed apart. */
+int mssm_token_logprobs_workspace(const mssm_logprob_dims* dims, int64_t* bytes);
 
 /*
  * Its gradient for dlogprobs (rows) fp32:
@@ -721,7 +726,7 @@ typedef struct {
 
 /*
  * Clipped policy loss with a KL term and its gradient, from one read of the
- * logits.  Per row, with logp as mssm_token_logprobs_fwd gives it:
+ * logits (two above a vocabulary of 65536).  Per row, with logp as mssm_token_logprobs_fwd gives it:
  *     ratio = exp(logp - old_logprobs)
  *     loss  = -min(ratio A, clip(ratio) A) + kl_coef (exp(x) - 1 - x),
  *     x = ref_logprobs - logp                 (an estimate of KL(policy || ref))
@@ -740,8 +745,8 @@ typedef struct {
  */
 int mssm_policy_loss(const void* logits, const int64_t* tokens, const float* old_logprobs,
                      const float* advantages, const float* ref_logprobs, const float* weights,
-                     float* loss, float* logprobs, void* dlogits, const mssm_policy_args* args,
-                     void* stream);
+                     float* loss, float* logprobs, void* dlogits, void* workspace,
+                     int64_t workspace_bytes, const mssm_policy_args* args, void* stream);
 
 typedef struct {
   int64_t rows;           /* 1 to 2^31 - 1                                    */

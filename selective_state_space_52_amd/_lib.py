@@ -40,7 +40,8 @@ EXPORTS = ("mssm_selective_scan_fwd", "mssm_selective_scan_bwd",
            "mssm_sample", "mssm_mamba2_state_update",
            "mssm_mamba2_state_update_workspace",
            "mssm_embedding_fwd", "mssm_embedding_bwd", "mssm_embedding_bwd_workspace",
-           "mssm_token_logprobs_fwd", "mssm_token_logprobs_bwd", "mssm_policy_loss",
+           "mssm_token_logprobs_fwd", "mssm_token_logprobs_workspace",
+           "mssm_token_logprobs_bwd", "mssm_policy_loss",
            "mssm_preference_loss", "mssm_adamw")
 
 
@@ -231,12 +232,12 @@ def lib():
         sig("mssm_embedding_fwd", [vp] * 3 + [ed, vp])
         sig("mssm_embedding_bwd", [vp] * 4 + [i64, ed, vp])
         sig("mssm_embedding_bwd_workspace", [ed, out64])
-        sig("mssm_token_logprobs_fwd", [vp] * 4 + [ld, vp])
+        sig("mssm_token_logprobs_fwd", [vp] * 5 + [i64, ld, vp])
+        sig("mssm_token_logprobs_workspace", [ld, out64])
         sig("mssm_token_logprobs_bwd", [vp] * 5 + [ld, vp])
-        sig("mssm_policy_loss", [vp] * 9 + [ctypes.POINTER(PolicyArgs), vp])
+        sig("mssm_policy_loss", [vp] * 10 + [i64, ctypes.POINTER(PolicyArgs), vp])
         sig("mssm_preference_loss", [vp] * 6 + [ctypes.POINTER(PreferenceArgs), vp])
-        sig("mssm_adamw", [ctypes.POINTER(AdamwTensor), i64] + [vp] * 4
-            + [ctypes.POINTER(AdamwArgs), vp])
+        sig("mssm_adamw", [vp, i64] + [vp] * 4 + [ctypes.POINTER(AdamwArgs), vp])
         _lib = L
     return _lib
 

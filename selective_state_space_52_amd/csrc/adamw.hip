@@ -146,14 +146,32 @@ __device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i
                               reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i));
 }
 
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return (uint64_t)hi << 32 | lo;
+}
+
 template <bool EIGHT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
-  // the tensor whose workgroup this is: the last that begins at or before it
+  // the tensor whose workgroup this is: the last that begins at or before it.
+  // Lane i holds the table's entry i, so that finding the tensor and reading its
+  // entry is one wait.
   const int lane = threadIdx.x & 63;
+  const int at_most = lane < p.count ? lane : p.count - 1;
+  const AdamTensor mine = p.tensors[at_most];
   const uint32_t first = lane < p.count ? p.first[lane] : 0xFFFFFFFFu;
   const int which = __popcll(__ballot(first <= blockIdx.x)) - 1;
-  const AdamTensor& t = p.tensors[which];
-  const int64_t begin = (int64_t)(blockIdx.x - p.first[which]) * kElements;
+  AdamTensor t;
+  t.param = (float*)of_lane((uint64_t)mine.param, which);
+  t.grad = (const void*)of_lane((uint64_t)mine.grad, which);
+  t.copy = (void*)of_lane((uint64_t)mine.copy, which);
+  t.size = (int64_t)of_lane((uint64_t)mine.size, which);
+  t.at = (int64_t)of_lane((uint64_t)mine.at, which);
+  t.decay = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.decay), which));
+  t.grad_bf16 = __builtin_amdgcn_readlane(mine.grad_bf16, which);
+  const uint32_t begins = (uint32_t)__builtin_amdgcn_readlane((int)first, which);
+  const int64_t begin = (int64_t)(blockIdx.x - begins) * kElements;
   const Rates r = rates_of(p);
   const float keep = 1.0f - r.lr * t.decay;
 #pragma unroll

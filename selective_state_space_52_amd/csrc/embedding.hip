@@ -82,16 +82,23 @@ __global__ void __launch_bounds__(kSortThreads)
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int first = blockIdx.x * range;
   const int mine = min(range, vocab - first);
-  for (int i = threadIdx.x; i < kSortWaves * range; i += kSortThreads) cursor[i] = 0;
-  __syncthreads();
-  // each wave takes a run of neighbouring tokens
+  // each wave takes a run of neighbouring tokens; the first batch stays
   const int run = ((rows + kSortThreads - 1) / kSortThreads) * 64;
   const int64_t begin = min((int64_t)rows, (int64_t)wave * run);
   const int64_t end = min((int64_t)rows, begin + run);
+  int64_t held[kBatch];
+  if (begin < end) load_tokens(held, tokens, begin + lane, end);
+  for (int i = threadIdx.x; i < kSortWaves * range; i += kSortThreads) cursor[i] = 0;
+  __syncthreads();
   uint32_t below = 0;
   for (int64_t i = begin; i < end; i += 64 * kBatch) {
     int64_t t[kBatch];
-    load_tokens(t, tokens, i + lane, end);
+    if (i == begin) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) t[b] = held[b];
+    } else {
+      load_tokens(t, tokens, i + lane, end);
+    }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (t[b] >= 0 && t[b] < first) ++below;
@@ -131,7 +138,12 @@ __global__ void __launch_bounds__(kSortThreads)
   __syncthreads();
   for (int64_t i = begin; i < end; i += 64 * kBatch) {
     int64_t t[kBatch];
-    load_tokens(t, tokens, i + lane, end);
+    if (i == begin) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) t[b] = held[b];
+    } else {
+      load_tokens(t, tokens, i + lane, end);
+    }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int64_t own = t[b] - first;
@@ -169,25 +181,20 @@ struct Pieces {
   U32Div chunks; // 16 bytes each, of a row of the gradient
 };
 
-template <bool TBF>
-__device__ __forceinline__ void finish(const EmbedBwdParams& p, int token, int col, float (&sum)[8]) {
-  const int n = p.dim - col;
-  const int64_t to = (int64_t)token * p.dim + col;
+// The token's row from its sum, and from what it held (ADD).
+template <bool TBF, bool ADD>
+__device__ __forceinline__ void finish(const EmbedBwdParams& p, int token, int col, float (&sum)[8],
+                                       const float (&old)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[j] *= p.scale;
-  if (p.add) {
-    float old[8];
-    load8<TBF>(old, p.dtable, to, n);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += old[j];
-  }
-  store8<TBF>(p.dtable, to, n, sum);
+  for (int j = 0; j < 8; ++j) sum[j] = ADD ? sum[j] * p.scale + old[j] : sum[j] * p.scale;
+  store8<TBF>(p.dtable, (int64_t)token * p.dim + col, p.dim - col, sum);
 }
 
 // Clears the rows that no token names, in pieces of 16 bytes: kClear a thread.
 constexpr int kClear = 16;
-template <bool TBF>
-__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, const Pieces& q, int64_t block) {
+template <bool TBF, typename Present>
+__device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, U32Div div, int64_t block,
+                                           Present present) {
   constexpr int kCols = TBF ? 8 : 4;
   typedef typename std::conditional<TBF, uint16_t, uint32_t>::type T;
   const int chunks = (p.dim + kCols - 1) / kCols;
@@ -196,11 +203,11 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, const Pieces
   const uint32_t at0 = (uint32_t)(first - row0 * chunks) + threadIdx.x;
 #pragma unroll 4
   for (int c = 0; c < kClear; ++c) {
-    const uint32_t at = at0 + c * kThreads, down = udiv(at, q.chunks);
+    const uint32_t at = at0 + c * kThreads, down = udiv(at, div);
     const int64_t row = row0 + down;
     if (row >= p.vocab) return;
     const int col = (int)(at - down * chunks) * kCols, n = p.dim - col;
-    if (q.present[row]) continue;
+    if (present(row, down)) continue;
     T* to = static_cast<T*>(p.dtable) + row * p.dim + col;
     if (n >= kCols) {
       *reinterpret_cast<Any16*>(to) = Any16{{0, 0, 0, 0}};
@@ -210,12 +217,15 @@ __device__ __forceinline__ void clear_rows(const EmbedBwdParams& p, const Pieces
   }
 }
 
+constexpr int kRows = 8;  // whose loads are in flight together
+
 // One wave a piece and slice of columns.  Its lanes hold the piece's rows and
 // tokens; 8 rows' loads are in flight together.
-template <bool TBF, bool OBF>
+template <bool TBF, bool OBF, bool ADD>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams p, Pieces q) {
   if ((int)blockIdx.x >= q.sums) {
-    clear_rows<TBF>(p, q, (int)blockIdx.x - q.sums);
+    clear_rows<TBF>(p, q.chunks, (int)blockIdx.x - q.sums,
+                    [&](int64_t row, uint32_t) { return q.present[row] != 0; });
     return;
   }
   const int64_t item = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
@@ -234,33 +244,28 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams 
   const int n = p.dim - col;
   const bool whole = n >= 8;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  int token = __builtin_amdgcn_readfirstlane(names);
-  constexpr int kRows = 8;
   for (int i = 0; i < len; i += kRows) {
     Raw8<OBF> raw[kRows];
+    Raw8<TBF> held_old[kRows];
     if (whole) {
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         const int64_t row = __builtin_amdgcn_readlane(rows, min(i + r, len - 1));
         raw[r] = load_raw8<OBF>(p.dout, row * p.io_stride + col);
       }
+      if constexpr (ADD) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          // what the row of a token that ends here holds
+          const int name = __builtin_amdgcn_readlane(names, min(i + r, len - 1));
+          if (i + r >= len - 1 || name != __builtin_amdgcn_readlane(names, i + r + 1))
+            held_old[r] = load_raw8<TBF>(p.dtable, (int64_t)name * p.dim + col);
+        }
+      }
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       if (i + r >= len) break;
-      const int next = __builtin_amdgcn_readlane(names, i + r);
-      if (next != token) {
-        if (n > 0) {
-          if (came_in)
-            store8<false>(q.head, piece * p.dim + col, n, sum);
-          else
-            finish<TBF>(p, token, col, sum);
-        }
-        came_in = false;
-        token = next;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-      }
       float v[8];
       if (whole)
         unpack8<OBF>(v, raw[r]);
@@ -270,22 +275,37 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams 
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      const bool last = i + r == len - 1;
+      const int token = __builtin_amdgcn_readlane(names, i + r);
+      if (!last && token == __builtin_amdgcn_readlane(names, i + r + 1)) continue;
+      if (n > 0) {
+        if (came_in) {
+          store8<false>(q.head, piece * p.dim + col, n, sum);
+        } else if (last && goes_on) {
+          store8<false>(q.tail, piece * p.dim + col, n, sum);
+        } else {
+          float old[8];
+          if constexpr (ADD) {
+            if (whole)
+              unpack8<TBF>(old, held_old[r]);
+            else
+              load8<TBF>(old, p.dtable, (int64_t)token * p.dim + col, n);
+          }
+          finish<TBF, ADD>(p, token, col, sum, old);
+        }
+      }
+      came_in = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
     }
   }
-  if (n <= 0) return;
-  if (came_in)
-    store8<false>(q.head, piece * p.dim + col, n, sum);
-  else if (goes_on)
-    store8<false>(q.tail, piece * p.dim + col, n, sum);
-  else
-    finish<TBF>(p, token, col, sum);
 }
 
 // The piece in which a token across pieces begins adds up its sums: a workgroup
 // for it and a slice of columns, whose waves take runs of the pieces, 8 loads in
 // flight, and are added in order.
 constexpr int kJoinWaves = kThreads / 64;
-template <bool TBF>
+template <bool TBF, bool ADD>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams p, Pieces q) {
   __shared__ float part[kJoinWaves][64][9];
   const int64_t piece = blockIdx.x / q.slices;
@@ -312,8 +332,10 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams
   const int64_t each = (pieces + kJoinWaves - 1) / kJoinWaves;
   const int64_t from = wave * each, to = min(pieces, from + each);
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  float old[8];
   if (n > 0) {
     if (wave == 0) load8<false>(sum, q.tail, piece * p.dim + col, n);
+    if (ADD && wave == 0) load8<TBF>(old, p.dtable, (int64_t)token * p.dim + col, n);
     const int64_t at = (piece + 1) * p.dim + col;
     int64_t i = from;
     for (; i + 8 <= to; i += 8) {
@@ -339,7 +361,118 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams
   for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += part[w][lane][j];
-  finish<TBF>(p, token, col, sum);
+  finish<TBF, ADD>(p, token, col, sum, old);
+}
+
+// Few rows: one launch and no order.  A workgroup takes a row and 512 columns and
+// compares the row's token with all others; where no earlier row has it, its
+// waves add up the rows that have it (in parts, added in order).
+constexpr int kDirect = 1024;
+template <bool TBF, bool OBF, bool ADD>
+__global__ void __launch_bounds__(kThreads)
+    embedding_direct_kernel(EmbedBwdParams p, int slices, int sums, U32Div chunks) {
+  __shared__ uint64_t same[kDirect / 64];
+  __shared__ float part[kJoinWaves][64][9];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int rows = (int)p.rows;
+  if ((int)blockIdx.x >= sums) {
+    __shared__ uint8_t named[kThreads * kClear + 8];
+    const int64_t block = (int)blockIdx.x - sums;
+    for (int i = threadIdx.x; i < kThreads * kClear + 8; i += kThreads) named[i] = 0;
+    __syncthreads();
+    constexpr int kCols = TBF ? 8 : 4;
+    const int64_t row0 = block * (kThreads * kClear) / ((p.dim + kCols - 1) / kCols);
+    for (int i = threadIdx.x; i < rows; i += kThreads) {
+      const int64_t at = p.tokens[i] - row0;
+      if (at >= 0 && at < kThreads * kClear + 8) named[at] = 1;
+    }
+    __syncthreads();
+    clear_rows<TBF>(p, chunks, block, [&](int64_t, uint32_t down) { return named[down] != 0; });
+    return;
+  }
+  const int row = (int)(blockIdx.x / slices);
+  const int col = (int)(blockIdx.x % slices) * 512 + lane * 8, n = p.dim - col;
+  const int64_t token = p.tokens[row];
+  if (token < 0 || token >= p.vocab) return;
+  const int words = (rows + 63) / 64;
+  for (int k = wave; k < words; k += kJoinWaves) {
+    const int i = k * 64 + lane;
+    const uint64_t m = __ballot(i < rows && p.tokens[min(i, rows - 1)] == token);
+    if (lane == 0) same[k] = m;
+  }
+  float old[8];
+  if (ADD && wave == 0 && n > 0) load8<TBF>(old, p.dtable, token * p.dim + col, n);
+  __syncthreads();
+  int total = 0;
+  for (int k = 0; k < words; ++k) total += __popcll(same[k]);
+  int before = __popcll(same[row >> 6] & ((1ull << (row & 63)) - 1));
+  for (int k = 0; k < row >> 6; ++k) before += __popcll(same[k]);
+  total = __builtin_amdgcn_readfirstlane(total);
+  if (__builtin_amdgcn_readfirstlane(before)) return;
+  const bool alone = total <= kRows;  // the first wave's
+  const int each = alone ? total : (total + kJoinWaves - 1) / kJoinWaves;
+  int left = min(each, total - wave * each);
+  if (alone && wave != 0) return;
+  // from this wave's first of the rows
+  int word = 0, skip = wave * each;
+  uint64_t bits = 0;
+  if (left > 0) {
+    bits = same[0];
+    while (skip >= __popcll(bits)) {
+      skip -= __popcll(bits);
+      bits = same[++word];
+    }
+    for (; skip > 0; --skip) bits &= bits - 1;
+  }
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  while (left > 0) {
+    const int now = min(left, kRows);
+    int at[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (r < now) {
+        while (bits == 0) bits = same[++word];
+        at[r] = word * 64 + __builtin_ctzll(bits);
+        bits &= bits - 1;
+      } else {
+        at[r] = at[r ? r - 1 : 0];
+      }
+    }
+    if (n >= 8) {
+      Raw8<OBF> raw[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        raw[r] = load_raw8<OBF>(p.dout, (int64_t)at[r] * p.io_stride + col);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= now) break;
+        float v[8];
+        unpack8<OBF>(v, raw[r]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
+    } else if (n > 0) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= now) break;
+        float v[8];
+        load8<OBF>(v, p.dout, (int64_t)at[r] * p.io_stride + col, n);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
+    }
+    left -= now;
+  }
+  if (!alone) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[wave][lane][j] = sum[j];
+    __syncthreads();
+    if (wave != 0) return;
+    for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += part[w][lane][j];
+  }
+  if (n > 0) finish<TBF, ADD>(p, (int)token, col, sum, old);
 }
 
 // Places of a piece: 8 at least, 64 (its wave's lanes) at most, in between as
@@ -370,48 +503,64 @@ hipError_t launch_embedding(const EmbedParams& p, bool table_bf16, bool io_bf16,
 }
 
 int64_t embedding_bwd_workspace(int64_t rows, int64_t vocab, int64_t dim) {
+  if (rows <= kDirect) return 0;
   return 256 + 2 * round256(rows * 4) + round256(vocab) +
          2 * round256(pieces_of(rows, dim) * dim * 4);
 }
 
-hipError_t launch_embedding_bwd(const EmbedBwdParams& p, bool table_bf16, bool io_bf16,
-                                hipStream_t st) {
+template <bool TBF, bool OBF, bool ADD>
+static hipError_t launch_bwd(const EmbedBwdParams& p, hipStream_t st) {
+  const int64_t chunks = TBF ? (p.dim + 7) / 8 : (p.dim + 3) / 4;
+  const int64_t clears = ADD ? 0 : (p.vocab * chunks + kThreads * kClear - 1) / (kThreads * kClear);
+  const U32Div div = make_u32div((uint32_t)chunks);
+  const int slices = (p.dim + 511) / 512;
+  if (p.rows <= kDirect) {
+    const int64_t sums = p.rows * slices;
+    hipLaunchKernelGGL((embedding_direct_kernel<TBF, OBF, ADD>), dim3((unsigned)(sums + clears)),
+                       dim3(kThreads), 0, st, p, slices, (int)sums, div);
+    return hipGetLastError();
+  }
   char* ws = static_cast<char*>(p.workspace);
-  Pieces q;
   int* count = reinterpret_cast<int*>(ws);
   ws += 256;
   int* order = reinterpret_cast<int*>(ws);
   ws += round256(p.rows * 4);
   int* named = reinterpret_cast<int*>(ws);
   ws += round256(p.rows * 4);
-  uint8_t* present = p.add ? nullptr : reinterpret_cast<uint8_t*>(ws);
+  uint8_t* present = ADD ? nullptr : reinterpret_cast<uint8_t*>(ws);
   ws += round256(p.vocab);
   const int64_t pieces = pieces_of(p.rows, p.dim);
+  Pieces q;
   q.head = reinterpret_cast<float*>(ws);
   q.tail = reinterpret_cast<float*>(ws + round256(pieces * p.dim * 4));
   q.order = order; q.named = named; q.count = count; q.present = present;
   q.len = len_of(p.rows, p.dim);
-  q.slices = (p.dim + 511) / 512;
-  const int64_t chunks = table_bf16 ? (p.dim + 7) / 8 : (p.dim + 3) / 4;
-  q.chunks = make_u32div((uint32_t)chunks);
+  q.slices = slices;
+  q.chunks = div;
   const SortPlan s = sort_plan(p.vocab);
-  const size_t lds = (size_t)kSortWaves * s.range * 4;
-  hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)s.groups), dim3(kSortThreads), lds, st,
-                     p.tokens, (int)p.rows, p.vocab, s.range, order, named, count, present);
+  hipLaunchKernelGGL(embedding_sort_kernel, dim3((unsigned)s.groups), dim3(kSortThreads),
+                     (size_t)kSortWaves * s.range * 4, st, p.tokens, (int)p.rows, p.vocab, s.range,
+                     order, named, count, present);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t per = kThreads / 64;
-  q.sums = (int)((pieces * q.slices + per - 1) / per);
-  const int64_t clears = p.add ? 0 : (p.vocab * chunks + kThreads * kClear - 1) / (kThreads * kClear);
-  const dim3 grid((unsigned)(q.sums + clears));
-  auto sum = table_bf16 ? (io_bf16 ? embedding_sum_kernel<true, true> : embedding_sum_kernel<true, false>)
-                        : (io_bf16 ? embedding_sum_kernel<false, true> : embedding_sum_kernel<false, false>);
-  hipLaunchKernelGGL(sum, grid, dim3(kThreads), 0, st, p, q);
+  q.sums = (int)((pieces * slices + per - 1) / per);
+  hipLaunchKernelGGL((embedding_sum_kernel<TBF, OBF, ADD>), dim3((unsigned)(q.sums + clears)),
+                     dim3(kThreads), 0, st, p, q);
   e = hipGetLastError();
-  if (e != hipSuccess || pieces == 1) return e;  // one piece: nothing goes on
-  auto join = table_bf16 ? embedding_join_kernel<true> : embedding_join_kernel<false>;
-  hipLaunchKernelGGL(join, dim3((unsigned)((pieces - 1) * q.slices)), dim3(kThreads), 0, st, p, q);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((embedding_join_kernel<TBF, ADD>), dim3((unsigned)((pieces - 1) * slices)),
+                     dim3(kThreads), 0, st, p, q);
   return hipGetLastError();
+}
+
+hipError_t launch_embedding_bwd(const EmbedBwdParams& p, bool table_bf16, bool io_bf16,
+                                hipStream_t st) {
+  if (p.add)
+    return table_bf16 ? (io_bf16 ? launch_bwd<true, true, true>(p, st) : launch_bwd<true, false, true>(p, st))
+                      : (io_bf16 ? launch_bwd<false, true, true>(p, st) : launch_bwd<false, false, true>(p, st));
+  return table_bf16 ? (io_bf16 ? launch_bwd<true, true, false>(p, st) : launch_bwd<true, false, false>(p, st))
+                    : (io_bf16 ? launch_bwd<false, true, false>(p, st) : launch_bwd<false, false, false>(p, st));
 }
 
 }  // namespace mssm

@@ -419,8 +419,11 @@ struct LogprobParams {
   int64_t rows, logits_stride, grad_stride;
   int32_t vocab;
   float inv_temperature, clip_lo, clip_hi, kl_coef;
+  float* partial;             // workspace: (rows, 2 parts + 1)
+  int32_t parts;              // of a long row, 0: whole rows; set by the launch
   int32_t past;               // the gradient is stored past the caches; set by the launch
 };
+int64_t logprob_workspace(int64_t rows, int64_t vocab);
 hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st);
 hipError_t launch_logprobs_bwd(LogprobParams p, bool bf16, hipStream_t st);
 

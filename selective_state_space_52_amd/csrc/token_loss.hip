@@ -58,8 +58,12 @@ __device__ __forceinline__ void opaque(Raw8<BF16> (&raw)[N]) {
 struct Running {
   float top, sum;
 };
+// Adds kFlight times 8 columns, as every kernel here does, so that a row's sum has
+// the same bits in all of them.
+constexpr int kFlight = 4;
 template <bool BF16, int N>
 __device__ __forceinline__ void take(Running& r, Raw8<BF16> (&raw)[N], float k) {
+  static_assert(N <= kFlight, "columns that are added together");
   float top = r.top;
 #pragma unroll
   for (int c = 0; c < N; ++c) {
@@ -81,21 +85,22 @@ __device__ __forceinline__ void take(Running& r, Raw8<BF16> (&raw)[N], float k) 
   r.sum = s;
 }
 
-// The workgroup's, from its threads'.
+// The wave's and the workgroup's, from their threads'.
+__device__ __forceinline__ Running of_wave(Running r, float k) {
+  float top = max16(r.top);
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  return Running{top, sum64(r.sum * hw_exp2((r.top - top) * k))};
+}
 template <int WAVES>
 __device__ __forceinline__ Running of_workgroup(Running r, float k) {
   __shared__ Running part[WAVES];
-  const float own = r.top;
-  float top = max16(own);
-  top = fmaxf(top, __shfl_xor(top, 16));
-  top = fmaxf(top, __shfl_xor(top, 32));
-  const float sum = sum64(r.sum * hw_exp2((own - top) * k));
-  if (WAVES == 1) return Running{top, sum};
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = Running{top, sum};
+  r = of_wave(r, k);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = r;
   __syncthreads();
   const int i = threadIdx.x & 15;
   r = part[i % WAVES];
-  top = max16(r.top);
+  const float top = max16(r.top);
   return Running{top, sum16(i < WAVES ? r.sum * hw_exp2((r.top - top) * k) : 0.0f)};
 }
 
@@ -104,7 +109,7 @@ struct Row {
   float top, log_sum, factor;
 };
 __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, bool live, Running r,
-                                          float taken) {
+                                          float taken, bool writes) {
   float logp = 0.0f, log_sum = 0.0f, loss = 0.0f, slope = 0.0f;
   if (live) {
     log_sum = logf(r.sum);
@@ -122,7 +127,7 @@ __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, b
       if (p.weights) slope *= p.weights[row];
     }
   }
-  if (threadIdx.x == 0) {
+  if (writes) {
     p.logprobs[row] = logp;
     if (p.loss) p.loss[row] = loss;
     if (p.stats) {
@@ -175,95 +180,148 @@ __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
   const int64_t token = p.tokens[row];
   const bool live = token >= 0 && token < p.vocab;
   const float k = p.inv_temperature * kLog2e;
-  Raw8<BF16> raw[NV];
+  constexpr int kGroups = (NV + kFlight - 1) / kFlight, kEach = NV / kGroups;
+  Raw8<BF16> raw[kGroups][kEach];
   Running r{kLowest, 0.0f};
   float taken = 0.0f;
   if (live) {
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-      raw[c] = load_columns<BF16>(p.logits, from, min((c * T + (int)threadIdx.x) * 8, p.vocab), p.vocab);
+      raw[c / kEach][c % kEach] = load_columns<BF16>(
+          p.logits, from, min((c * T + (int)threadIdx.x) * 8, p.vocab), p.vocab);
     taken = logit<BF16>(p.logits, from + token);
-    take<BF16, NV>(r, raw, k);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) take<BF16, kEach>(r, raw[g], k);
     r = of_workgroup<T / 64>(r, k);
   }
-  const Row w = finish_row(p, row, live, r, taken);
+  const Row w = finish_row(p, row, live, r, taken, threadIdx.x == 0);
   if (!p.dlogits) return;
   if (w.factor == 0.0f) {
     store_zeros<BF16>(p, to, threadIdx.x * 8, p.vocab, T * 8);
     return;
   }
-  if constexpr (BF16) opaque(raw);
+  if constexpr (BF16) {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) opaque(raw[g]);
+  }
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int i = (c * T + threadIdx.x) * 8;
-    if (i < p.vocab) store_slope<BF16>(p, to, i, (int)token, raw[c], w, k);
+    if (i < p.vocab) store_slope<BF16>(p, to, i, (int)token, raw[c / kEach][c % kEach], w, k);
   }
 }
 
-// One workgroup a longer row, which is read again for its gradient.
-constexpr int kThreads = 1024, kFlight = 4;
+// One workgroup a row of which nothing is kept: without the gradient.
+constexpr int kThreads = 1024;
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobParams p) {
-  const int64_t row = blockIdx.x, from = row * p.logits_stride, to = row * p.grad_stride;
+  const int64_t row = blockIdx.x, from = row * p.logits_stride;
   const int64_t token = p.tokens[row];
   const bool live = token >= 0 && token < p.vocab;
   const float k = p.inv_temperature * kLog2e;
   Running r{kLowest, 0.0f};
   float taken = 0.0f;
-  Raw8<BF16> raw[kFlight];
-  const auto load = [&](int i) {
-#pragma unroll
-    for (int c = 0; c < kFlight; ++c)
-      raw[c] = load_columns<BF16>(p.logits, from, min(i + c * kThreads * 8, p.vocab), p.vocab);
-  };
   if (live) {
     for (int i = threadIdx.x * 8; i < p.vocab; i += kFlight * kThreads * 8) {
-      load(i);
+      Raw8<BF16> raw[kFlight];
+#pragma unroll
+      for (int c = 0; c < kFlight; ++c)
+        raw[c] = load_columns<BF16>(p.logits, from, min(i + c * kThreads * 8, p.vocab), p.vocab);
       take<BF16, kFlight>(r, raw, k);
     }
     taken = logit<BF16>(p.logits, from + token);
     r = of_workgroup<kThreads / 64>(r, k);
   }
-  const Row w = finish_row(p, row, live, r, taken);
-  if (!p.dlogits) return;
-  if (w.factor == 0.0f) {
-    store_zeros<BF16>(p, to, threadIdx.x * 8, p.vocab, kThreads * 8);
-    return;
-  }
-  for (int i = threadIdx.x * 8; i < p.vocab; i += kFlight * kThreads * 8) {
-    load(i);
-#pragma unroll
-    for (int c = 0; c < kFlight; ++c) {
-      const int at = i + c * kThreads * 8;
-      if (at < p.vocab) store_slope<BF16>(p, to, at, (int)token, raw[c], w, k);
-    }
-  }
+  finish_row(p, row, live, r, taken, threadIdx.x == 0);
 }
 
-// The gradient alone: a workgroup takes kColumns columns of a row.
-constexpr int kBwdThreads = 256, kBwdFlight = 4, kColumns = kBwdThreads * 8 * kBwdFlight;
+// ---- Longer rows: parts of them by workgroups of their own, whose sums a second
+// launch joins and, for the gradient, reads the logits again.
+constexpr int kPartThreads = 256, kColumns = kPartThreads * 8 * kFlight;
+
+// A workgroup sums `turns` times kColumns columns; the first of a row keeps the
+// token's logit too (the gradient may take the logits' place).
 template <bool BF16>
-__global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(LogprobParams p, int parts) {
-  const int64_t row = blockIdx.x / parts;
-  const int first = (int)(blockIdx.x % parts) * kColumns + threadIdx.x * 8;
-  const int end = min(p.vocab, (int)(blockIdx.x % parts) * kColumns + kColumns);
+__global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParams p, int turns) {
+  const int64_t row = blockIdx.x / p.parts, from = row * p.logits_stride;
+  const int part = (int)(blockIdx.x % p.parts);
+  const int64_t token = p.tokens[row];
+  if (token < 0 || token >= p.vocab) return;
+  const float k = p.inv_temperature * kLog2e;
+  Running r{kLowest, 0.0f};
+  const int first = part * turns * kColumns + threadIdx.x * 8;
+  for (int t = 0; t < turns; ++t) {
+    Raw8<BF16> raw[kFlight];
+#pragma unroll
+    for (int c = 0; c < kFlight; ++c)
+      raw[c] = load_columns<BF16>(
+          p.logits, from, min(first + t * kColumns + c * kPartThreads * 8, p.vocab), p.vocab);
+    take<BF16, kFlight>(r, raw, k);
+  }
+  r = of_workgroup<kPartThreads / 64>(r, k);
+  if (threadIdx.x != 0) return;
+  float* out = p.partial + row * (2 * p.parts + 1);
+  out[2 * part] = r.top;
+  out[2 * part + 1] = r.sum;
+  if (part == 0) out[2 * p.parts] = logit<BF16>(p.logits, from + token);
+}
+
+// The row's, by a wave.
+__device__ __forceinline__ Running join_parts(const LogprobParams& p, int64_t row, float k) {
+  const float* in = p.partial + row * (2 * p.parts + 1);
+  Running r{kLowest, 0.0f};
+  for (int i = threadIdx.x & 63; i < p.parts; i += 64) {
+    const Running o{in[2 * i], in[2 * i + 1]};
+    const float top = fmaxf(r.top, o.top);
+    r = Running{top, r.sum * hw_exp2((r.top - top) * k) + o.sum * hw_exp2((o.top - top) * k)};
+  }
+  return of_wave(r, k);
+}
+
+// Without the gradient: a wave a row.
+__global__ void __launch_bounds__(kPartThreads) logprob_join_kernel(LogprobParams p) {
+  const int64_t row = (int64_t)blockIdx.x * (kPartThreads / 64) + (threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const int64_t token = p.tokens[row];
+  const bool live = token >= 0 && token < p.vocab;
+  Running r{kLowest, 0.0f};
+  if (live) r = join_parts(p, row, p.inv_temperature * kLog2e);
+  finish_row(p, row, live, r, live ? p.partial[row * (2 * p.parts + 1) + 2 * p.parts] : 0.0f,
+             (threadIdx.x & 63) == 0);
+}
+
+// The gradient: a workgroup takes kColumns columns of a row, whose statistics it
+// has from the forward call (STATS) or joins.
+template <bool BF16, bool STATS>
+__global__ void __launch_bounds__(kPartThreads) logprob_bwd_kernel(LogprobParams p, int pieces) {
+  const int64_t row = blockIdx.x / pieces;
+  const int piece = (int)(blockIdx.x % pieces);
+  const int first = piece * kColumns + threadIdx.x * 8, end = min(p.vocab, (piece + 1) * kColumns);
   const int64_t token = p.tokens[row], from = row * p.logits_stride, to = row * p.grad_stride;
   const bool live = token >= 0 && token < p.vocab;
-  const Row w{p.stats[2 * row], p.stats[2 * row + 1],
-              live ? p.dlogprobs[row] * p.inv_temperature : 0.0f};
+  const float k = p.inv_temperature * kLog2e;
+  Row w;
+  if constexpr (STATS) {
+    w = Row{p.stats[2 * row], p.stats[2 * row + 1],
+            live ? p.dlogprobs[row] * p.inv_temperature : 0.0f};
+  } else {
+    Running r{kLowest, 0.0f};
+    if (live) r = join_parts(p, row, k);
+    w = finish_row(p, row, live, r, live ? p.partial[row * (2 * p.parts + 1) + 2 * p.parts] : 0.0f,
+                   piece == 0 && threadIdx.x == 0);
+  }
   if (w.factor == 0.0f) {
-    store_zeros<BF16>(p, to, first, end, kBwdThreads * 8);
+    store_zeros<BF16>(p, to, first, end, kPartThreads * 8);
     return;
   }
-  Raw8<BF16> raw[kBwdFlight];
+  Raw8<BF16> raw[kFlight];
 #pragma unroll
-  for (int c = 0; c < kBwdFlight; ++c)
-    raw[c] = load_columns<BF16>(p.logits, from, min(first + c * kBwdThreads * 8, p.vocab), p.vocab);
+  for (int c = 0; c < kFlight; ++c)
+    raw[c] = load_columns<BF16>(p.logits, from, min(first + c * kPartThreads * 8, p.vocab), p.vocab);
 #pragma unroll
-  for (int c = 0; c < kBwdFlight; ++c) {
-    const int i = first + c * kBwdThreads * 8;
-    if (i < end)
-      store_slope<BF16>(p, to, i, (int)token, raw[c], w, p.inv_temperature * kLog2e);
+  for (int c = 0; c < kFlight; ++c) {
+    const int i = first + c * kPartThreads * 8;
+    if (i < end) store_slope<BF16>(p, to, i, (int)token, raw[c], w, k);
   }
 }
 
@@ -307,30 +365,51 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(PreferencePara
 
 }  // namespace
 
+// Columns that a workgroup of 1024 threads can hold.
+constexpr int64_t kHeld = 1024 * 8 * 8;
+
+// Turns of a part: one, or as many (up to 8) as leave 2048 workgroups.
+static int turns_of(int64_t rows, int64_t vocab) {
+  const int64_t turns = rows * ((vocab + kColumns - 1) / kColumns) / 2048;
+  return (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns);
+}
+static int parts_of(int64_t rows, int64_t vocab) {
+  const int64_t each = (int64_t)turns_of(rows, vocab) * kColumns;
+  return vocab <= kHeld ? 0 : (int)((vocab + each - 1) / each);
+}
+int64_t logprob_workspace(int64_t rows, int64_t vocab) {
+  const int64_t parts = parts_of(rows, vocab);
+  return parts ? rows * (2 * parts + 1) * 4 : 0;
+}
+
 template <bool BF16>
-static void launch_row(const LogprobParams& p, hipStream_t st) {
+static hipError_t launch_row(const LogprobParams& p, hipStream_t st) {
   const dim3 grid((unsigned)p.rows);
-  if (!p.dlogits && p.vocab > 16384) {
-    hipLaunchKernelGGL((logprob_kernel<BF16>), grid, dim3(kThreads), 0, st, p);
-    return;
-  }
   const auto go = [&](auto kernel, int threads) {
     hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, p);
+    return hipGetLastError();
   };
-  if (p.vocab <= 256 * 8)
-    go(logprob_held_kernel<BF16, 256, 1>, 256);
-  else if (p.vocab <= 256 * 8 * 2)
-    go(logprob_held_kernel<BF16, 256, 2>, 256);
-  else if (p.vocab <= 256 * 8 * 4)
-    go(logprob_held_kernel<BF16, 256, 4>, 256);
-  else if (p.vocab <= 1024 * 8 * 2)
-    go(logprob_held_kernel<BF16, 1024, 2>, 1024);
-  else if (p.vocab <= 1024 * 8 * 4)
-    go(logprob_held_kernel<BF16, 1024, 4>, 1024);
-  else if (p.vocab <= 1024 * 8 * 8)
-    go(logprob_held_kernel<BF16, 1024, 8>, 1024);
-  else
-    go(logprob_kernel<BF16>, kThreads);
+  if (p.parts) {
+    hipLaunchKernelGGL(logprob_part_kernel<BF16>, dim3((unsigned)(p.rows * p.parts)),
+                       dim3(kPartThreads), 0, st, p, turns_of(p.rows, p.vocab));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int pieces = (p.vocab + kColumns - 1) / kColumns;
+    if (p.dlogits)
+      hipLaunchKernelGGL((logprob_bwd_kernel<BF16, false>), dim3((unsigned)(p.rows * pieces)),
+                         dim3(kPartThreads), 0, st, p, pieces);
+    else
+      hipLaunchKernelGGL(logprob_join_kernel, dim3((unsigned)((p.rows + 3) / 4)),
+                         dim3(kPartThreads), 0, st, p);
+    return hipGetLastError();
+  }
+  if (p.vocab <= 256 * 8) return go(logprob_held_kernel<BF16, 256, 1>, 256);
+  if (p.vocab <= 256 * 8 * 2) return go(logprob_held_kernel<BF16, 256, 2>, 256);
+  if (p.vocab <= 256 * 8 * 4) return go(logprob_held_kernel<BF16, 256, 4>, 256);
+  if (p.vocab <= 1024 * 8 * 2) return go(logprob_held_kernel<BF16, 1024, 2>, 1024);
+  if (!p.dlogits) return go(logprob_kernel<BF16>, kThreads);
+  if (p.vocab <= 1024 * 8 * 4) return go(logprob_held_kernel<BF16, 1024, 4>, 1024);
+  return go(logprob_held_kernel<BF16, 1024, 8>, 1024);
 }
 
 // Gradients of more than 64 MB go past the caches, which would be left full of
@@ -341,16 +420,15 @@ static bool goes_past(const LogprobParams& p, bool bf16) {
 
 hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st) {
   p.past = goes_past(p, bf16);
-  bf16 ? launch_row<true>(p, st) : launch_row<false>(p, st);
-  return hipGetLastError();
+  p.parts = parts_of(p.rows, p.vocab);
+  return bf16 ? launch_row<true>(p, st) : launch_row<false>(p, st);
 }
 
 hipError_t launch_logprobs_bwd(LogprobParams p, bool bf16, hipStream_t st) {
   p.past = goes_past(p, bf16);
-  const int64_t parts = (p.vocab + kColumns - 1) / kColumns;
-  auto kernel = bf16 ? logprob_bwd_kernel<true> : logprob_bwd_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(p.rows * parts)), dim3(kBwdThreads), 0, st, p,
-                     (int)parts);
+  const int pieces = (p.vocab + kColumns - 1) / kColumns;
+  auto kernel = bf16 ? logprob_bwd_kernel<true, true> : logprob_bwd_kernel<false, true>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(p.rows * pieces)), dim3(kPartThreads), 0, st, p, pieces);
   return hipGetLastError();
 }
 

@@ -21,9 +21,9 @@ int check_embed_dims(const mssm_embed_dims* d) {
     return MSSM_ERR_DIMS;
   if (d->io_stride != 0 && (d->io_stride < d->dim || !fits(d->rows, d->io_stride)))
     return MSSM_ERR_DIMS;
-  // at most one wave for each 512 columns of a row, in both directions, and in
+  // at most a workgroup for each 512 columns of a row of few, a wave of many, and in
   // the backward a thread for 64 columns of the table
-  if (!fits(d->rows, (d->dim + 511) / 512 * 64, kItems / 2) ||
+  if (!fits(d->rows, (d->dim + 511) / 512 * 64, kItems / 4) ||
       !fits(d->vocab, (d->dim + 3) / 4, kItems / 2 * 16 - 4096))
     return MSSM_ERR_DIMS;
   return MSSM_OK;
@@ -39,8 +39,8 @@ int check_logprob_dims(const mssm_logprob_dims* d, bool grad) {
   if (grad && d->grad_stride != 0 &&
       (d->grad_stride < d->vocab || !fits(d->rows, d->grad_stride)))
     return MSSM_ERR_DIMS;
-  // the backward's workgroups of 256 threads take 8192 columns
-  if (grad && !fits(d->rows, (d->vocab + 8191) / 8192, kItems / 256)) return MSSM_ERR_DIMS;
+  // workgroups of 256 threads take 8192 columns
+  if (!fits(d->rows, (d->vocab + 8191) / 8192, kItems / 256)) return MSSM_ERR_DIMS;
   if (!(d->temperature > 0.0f) || !std::isfinite(1.0f / d->temperature) ||
       1.0f / d->temperature == 0.0f)
     return MSSM_ERR_DIMS;
@@ -127,19 +127,31 @@ int mssm_embedding_bwd(const int64_t* tokens, const void* dout, void* dtable, vo
               "embedding backward launch");
 }
 
-int mssm_token_logprobs_fwd(const void* logits, const int64_t* tokens, float* logprobs,
-                            float* stats, const mssm_logprob_dims* dims, void* stream) {
+int mssm_token_logprobs_workspace(const mssm_logprob_dims* dims, int64_t* bytes) {
+  if (!bytes) return MSSM_ERR_NULL;
   const int rc = check_logprob_dims(dims, false);
+  if (rc != MSSM_OK) return rc;
+  *bytes = mssm::logprob_workspace(dims->rows, dims->vocab);
+  return MSSM_OK;
+}
+
+int mssm_token_logprobs_fwd(const void* logits, const int64_t* tokens, float* logprobs,
+                            float* stats, void* workspace, int64_t workspace_bytes,
+                            const mssm_logprob_dims* dims, void* stream) {
+  int rc = check_logprob_dims(dims, false);
   if (rc != MSSM_OK) return rc;
   if (!logits || !tokens || !logprobs) return MSSM_ERR_NULL;
   if (!aligned(logits, size_of(dims->io_dtype)) || !aligned(tokens, 8) ||
       !all_aligned({logprobs, stats}, 4))
     return MSSM_ERR_ALIGN;
-  const int64_t rows = dims->rows;
-  if (aliased({range(logprobs, rows * 4), range(stats, rows * 8)},
+  const int64_t rows = dims->rows, need = mssm::logprob_workspace(rows, dims->vocab);
+  if (aliased({range(logprobs, rows * 4), range(stats, rows * 8), range(workspace, need)},
               {logit_ranges(logits, nullptr, dims).logits, range(tokens, rows * 8)}))
     return MSSM_ERR_ALIAS;
+  rc = mssm::check_workspace(workspace, workspace_bytes, need);
+  if (rc != MSSM_OK) return rc;
   mssm::LogprobParams p = logprob_params(dims);
+  p.partial = static_cast<float*>(workspace);
   p.logits = logits; p.tokens = tokens; p.logprobs = logprobs; p.stats = stats;
   return done(mssm::launch_logprobs(p, dims->io_dtype == MSSM_BF16, (hipStream_t)stream),
               "log-probability launch");
@@ -168,11 +180,11 @@ int mssm_token_logprobs_bwd(const void* logits, const int64_t* tokens, const flo
 
 int mssm_policy_loss(const void* logits, const int64_t* tokens, const float* old_logprobs,
                      const float* advantages, const float* ref_logprobs, const float* weights,
-                     float* loss, float* logprobs, void* dlogits, const mssm_policy_args* args,
-                     void* stream) {
+                     float* loss, float* logprobs, void* dlogits, void* workspace,
+                     int64_t workspace_bytes, const mssm_policy_args* args, void* stream) {
   if (!args) return MSSM_ERR_NULL;
   const mssm_logprob_dims* d = &args->dims;
-  const int rc = check_logprob_dims(d, dlogits != nullptr);
+  int rc = check_logprob_dims(d, dlogits != nullptr);
   if (rc != MSSM_OK) return rc;
   if (!(args->clip_low >= 0.0f) || !(args->clip_high >= 0.0f) || !(args->kl_coef >= 0.0f) ||
       !std::isfinite(args->kl_coef))
@@ -188,11 +200,16 @@ int mssm_policy_loss(const void* logits, const int64_t* tokens, const float* old
   const Range r_tok = range(tokens, rows * 8), r_old = range(old_logprobs, rows * 4);
   const Range r_adv = range(advantages, rows * 4), r_ref = range(ref_logprobs, rows * 4);
   const Range r_w = range(weights, rows * 4);
-  if (aliased({r_loss, r_logp}, {r.logits, r_tok, r_old, r_adv, r_ref, r_w}) ||
-      aliased({r.grad, r_loss, r_logp},
+  const int64_t need = mssm::logprob_workspace(rows, d->vocab);
+  const Range r_ws = range(workspace, need);
+  if (aliased({r_loss, r_logp, r_ws}, {r.logits, r_tok, r_old, r_adv, r_ref, r_w}) ||
+      aliased({r.grad, r_loss, r_logp, r_ws},
               {r.in_place ? Range{0, 0} : r.logits, r_tok, r_old, r_adv, r_ref, r_w}))
     return MSSM_ERR_ALIAS;
+  rc = mssm::check_workspace(workspace, workspace_bytes, need);
+  if (rc != MSSM_OK) return rc;
   mssm::LogprobParams p = logprob_params(d);
+  p.partial = static_cast<float*>(workspace);
   p.logits = logits; p.tokens = tokens; p.logprobs = logprobs;
   p.old_logprobs = old_logprobs; p.advantages = advantages; p.ref_logprobs = ref_logprobs;
   p.weights = weights; p.loss = loss; p.dlogits = dlogits;

@@ -7,12 +7,11 @@ device pointers and the current HIP stream passed on.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 import torch
 
-from ._lib import (MSSM_BF16, MSSM_F32, AdamwArgs, AdamwTensor, EmbedDims, LogprobDims, PolicyArgs,
-                   PreferenceArgs, lib)
+from ._lib import AdamwArgs, EmbedDims, LogprobDims, PolicyArgs, PreferenceArgs, lib
 from .layer import _IO, F8, _call, _empty, _io, _is, _ptr, _rows, _size
 
 __all__ = ["embedding_fwd", "embedding_bwd", "token_logprobs_fwd", "token_logprobs_bwd",
@@ -23,6 +22,10 @@ def _dtype(dtype, name):
     if dtype not in _IO:
         raise ValueError("%s must be float32 or bfloat16" % name)
     return _IO[dtype]
+
+
+def _empty1(n, device):
+    return torch.empty_strided((n,), (1,), dtype=torch.float32, device=device)
 
 
 def _tokens(tokens, device=None):
@@ -52,6 +55,10 @@ def embedding_fwd(tokens, table, scale=1.0, out_dtype=None):
     return out
 
 
+# The most rows whose gradient needs no workspace.
+_UNSORTED = 1024
+
+
 def embedding_bwd(tokens, dout, vocab, scale=1.0, out_dtype=torch.float32, add_to=None):
     """The table's gradient for dout (rows, dim) = dLoss/d(embedding_fwd), fp32 or
     bf16 with contiguous rows: scale times the sum of each token's rows.
@@ -72,10 +79,10 @@ def embedding_bwd(tokens, dout, vocab, scale=1.0, out_dtype=torch.float32, add_t
         t = _io(add_to, "add_to", 2)
         _is(add_to, "add_to", add_to.dtype, (vocab, dim), dev)
     dims = EmbedDims(rows, vocab, dim, stride, t, io, scale, int(add_to is not None))
-    need = _size(lib().mssm_embedding_bwd_workspace, dims, dev)
+    need = 0 if rows <= _UNSORTED else _size(lib().mssm_embedding_bwd_workspace, dims, dev)
     out = _empty(vocab, dim, out_dtype, dev) if add_to is None else add_to
     # from torch's caching allocator: ordered on the current stream, 512-byte aligned
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call(dev, lib().mssm_embedding_bwd, _ptr(tokens), _ptr(dout), _ptr(out), _ptr(ws), need, dims)
     return out
 
@@ -96,6 +103,18 @@ def _logits(logits, tokens, temperature, out=None):
     return LogprobDims(rows, vocab, stride, grad_stride, io, temperature)
 
 
+# The longest rows whose sums need no workspace.
+_WHOLE = 65536
+
+
+def _parts(dims, device):
+    """(workspace, bytes) of a call that sums rows of this length."""
+    if dims.vocab <= _WHOLE:
+        return None, 0
+    need = _size(lib().mssm_token_logprobs_workspace, dims, device)
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
 def token_logprobs_fwd(logits, tokens, temperature=1.0):
     """Log-probabilities of tokens (rows,) int64 under softmax(logits /
     temperature); logits: (rows, vocab) fp32 or bf16 with contiguous rows.
@@ -105,10 +124,11 @@ def token_logprobs_fwd(logits, tokens, temperature=1.0):
     which token_logprobs_bwd needs)."""
     dims = _logits(logits, tokens, temperature)
     dev, rows = logits.device, logits.shape[0]
-    logprobs = torch.empty(rows, dtype=torch.float32, device=dev)
+    logprobs = _empty1(rows, dev)
     stats = _empty(rows, 2, torch.float32, dev)
+    ws, need = _parts(dims, dev)
     _call(dev, lib().mssm_token_logprobs_fwd, _ptr(logits), _ptr(tokens), _ptr(logprobs),
-          _ptr(stats), dims)
+          _ptr(stats), _ptr(ws), need, dims)
     return logprobs, stats
 
 
@@ -154,12 +174,12 @@ def policy_loss(logits, tokens, old_logprobs, advantages, ref_logprobs=None, wei
         _vector(weights, "weights", rows, dev)
     if want_grad and out is None:
         out = _empty(rows, vocab, logits.dtype, dev)
-    loss = torch.empty(rows, dtype=torch.float32, device=dev)
-    logprobs = torch.empty(rows, dtype=torch.float32, device=dev)
+    loss, logprobs = _empty1(rows, dev), _empty1(rows, dev)
+    ws, need = _parts(dims, dev)
     args = PolicyArgs(dims, clip_low, clip_high, kl_coef, 0)
     _call(dev, lib().mssm_policy_loss, _ptr(logits), _ptr(tokens), _ptr(old_logprobs),
           _ptr(advantages), _ptr(ref_logprobs), _ptr(weights), _ptr(loss), _ptr(logprobs),
-          _ptr(out), args)
+          _ptr(out), _ptr(ws), need, args)
     return loss, logprobs, out
 
 
@@ -184,8 +204,7 @@ def preference_loss(logprobs, ref_logprobs, offsets, weights=None, beta=0.1, lab
     _is(offsets, "offsets", torch.int32, offsets.shape, dev)
     if weights is not None:
         _vector(weights, "weights", pairs, dev)
-    loss = torch.empty(pairs, dtype=torch.float32, device=dev)
-    dlogprobs = torch.empty(rows, dtype=torch.float32, device=dev)
+    loss, dlogprobs = _empty1(pairs, dev), _empty1(rows, dev)
     args = PreferenceArgs(rows, pairs, beta, label_smoothing)
     _call(dev, lib().mssm_preference_loss, _ptr(logprobs), _ptr(ref_logprobs), _ptr(offsets),
           _ptr(weights), _ptr(loss), _ptr(dlogprobs), args)
@@ -220,6 +239,28 @@ def _one(v, name, dtype, device):
     return v.data_ptr()
 
 
+def _plain(tensors, device):
+    """Whether all are contiguous and on this device."""
+    n = len(tensors)
+    return (list(map(torch.Tensor.get_device, tensors)).count(device.index) == n
+            and list(map(torch.Tensor.is_contiguous, tensors)).count(True) == n)
+
+
+def _refuse_tensors(params, grads, device):
+    for i, (p, g) in enumerate(zip(params, grads)):
+        _is(p, "params[%d]" % i, torch.float32, p.shape, device)
+        _io(g, "grads[%d]" % i, p.dim())
+        _is(g, "grads[%d]" % i, g.dtype, p.shape, device)
+    raise ValueError("params and grads do not fit together")
+
+
+def _copies(copies, params, device):
+    for i, (c, p) in enumerate(zip(copies, params)):
+        if c is not None:
+            _is(c, "copies[%d]" % i, torch.bfloat16, p.shape, device)
+    return [0 if c is None else c.data_ptr() for c in copies]
+
+
 def adamw_step(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01,
                m_scales=None, v_scales=None, copies=None, grad_scale=1.0, seed=0):
     """AdamW step of many tensors, in place, in one launch for each 64 of them.
@@ -235,30 +276,27 @@ def adamw_step(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weig
     count = len(params)
     if count == 0 or len(grads) != count or (copies is not None and len(copies) != count):
         raise ValueError("params, grads and copies must be lists of the same length, not empty")
-    f32, bf16 = torch.float32, torch.bfloat16
+    f32 = torch.float32
     dev = params[0].device
     if not params[0].is_cuda:
         raise ValueError("params[0] must be a GPU tensor")
-    table = (AdamwTensor * count)()
     decays = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
     if len(decays) != count:
         raise ValueError("weight_decay must be a number or one for each tensor")
-    blocks = 0
-    for i in range(count):
-        p, g = params[i], grads[i]
-        if p.dtype is not f32 or p.device != dev or not p.is_contiguous():
-            _is(p, "params[%d]" % i, f32, p.shape, dev)
-        if g.shape != p.shape or g.device != dev or not g.is_contiguous() or g.dtype not in _IO:
-            _io(g, "grads[%d]" % i, p.dim())
-            _is(g, "grads[%d]" % i, g.dtype, p.shape, dev)
-        c = None if copies is None else copies[i]
-        if c is not None:
-            _is(c, "copies[%d]" % i, bf16, p.shape, dev)
-            c = c.data_ptr()
-        n = p.numel()
-        blocks += (n + 127) >> 7
-        table[i] = (p.data_ptr(), g.data_ptr(), c, n, decays[i],
-                    MSSM_F32 if g.dtype is f32 else MSSM_BF16)
+    # lists and maps: half the time of a loop over the tensors
+    codes = list(map(_IO.get, [g.dtype for g in grads]))
+    if not (_plain(params, dev) and _plain(grads, dev) and None not in codes
+            and [p.dtype for p in params].count(f32) == count
+            and [p.shape for p in params] == [g.shape for g in grads]):
+        _refuse_tensors(params, grads, dev)
+    sizes = list(map(torch.Tensor.numel, params))
+    blocks = sum([(n + 127) >> 7 for n in sizes])
+    flat = [None] * (6 * count)     # mssm_adamw_tensor's fields
+    flat[0::6] = map(torch.Tensor.data_ptr, params)
+    flat[1::6] = map(torch.Tensor.data_ptr, grads)
+    flat[2::6] = [0] * count if copies is None else _copies(copies, params, dev)
+    flat[3::6], flat[4::6], flat[5::6] = sizes, decays, codes
+    table = struct.pack("PPPqfi" * count, *flat)
     eight = m.dtype is F8
     for t, name in ((m, "m"), (v, "v")):
         _is(t, name, F8 if eight else f32, (blocks * 128,), dev)

@@ -59,7 +59,9 @@ def test_embedding_backward(L):
         q = {**p, **o}
         return L.mssm_embedding_bwd(*[q[n] for n in names], size, dims or _embed(), None)
     n = ctypes.c_int64(0)
-    assert L.mssm_embedding_bwd_workspace(_embed(), n) == 0 and n.value > 0
+    assert L.mssm_embedding_bwd_workspace(_embed(rows=1024), n) == 0 and n.value == 0
+    many = dict(rows=1025)
+    assert L.mssm_embedding_bwd_workspace(_embed(**many), n) == 0 and n.value > 0
     need = n.value
     assert L.mssm_embedding_bwd_workspace(_embed(), None) == NULL
     assert L.mssm_embedding_bwd_workspace(None, n) == NULL
@@ -72,10 +74,11 @@ def test_embedding_backward(L):
     assert call(dout=p["dout"] + 1) == ALIGN
     assert call(dtable=p["dtable"] + 2) == ALIGN
     assert call(dtable=p["dout"] + 16 * 64 * 2 - 4) == ALIAS
-    assert call(ws=p["dtable"]) == ALIAS
-    assert call(ws=p["tokens"] - 256) == ALIAS
-    assert call(ws=None) == WORKSPACE and call(size=need - 1) == WORKSPACE
-    assert call(ws=p["ws"] + 16) == WORKSPACE
+    assert call(_embed(**many), ws=p["dtable"]) == ALIAS
+    assert call(_embed(**many), ws=p["tokens"] - 256) == ALIAS
+    assert call(_embed(**many), ws=None) == WORKSPACE
+    assert call(_embed(**many), size=need - 1) == WORKSPACE
+    assert call(_embed(**many), ws=p["ws"] + 16) == WORKSPACE
 
 
 def _logp(rows=4, vocab=1000, ls=0, gs=0, io=BF16, t=1.0):
@@ -94,8 +97,9 @@ def test_token_logprobs(L):
 
     def call(dims=None, **o):
         q = {**p, **o}
-        return L.mssm_token_logprobs_fwd(*[q[n] for n in names], dims or _logp(), None)
-    assert L.mssm_token_logprobs_fwd(*p.values(), None, None) == NULL
+        return L.mssm_token_logprobs_fwd(*[q[n] for n in names], ws, size, dims or _logp(), None)
+    ws, size = None, 0
+    assert L.mssm_token_logprobs_fwd(*p.values(), None, 0, None, None) == NULL
     for n in names[:3]:
         assert call(**{n: None}) == NULL, n
     for bad in BAD_LOGP:
@@ -106,6 +110,20 @@ def test_token_logprobs(L):
     assert call(stats=p["stats"] + 2) == ALIGN
     assert call(stats=p["logprobs"] + 12) == ALIAS
     assert call(logprobs=p["logits"] + 4 * 1000 * 2 - 4) == ALIAS
+    # the workspace of long rows
+    n = ctypes.c_int64(-1)
+    assert L.mssm_token_logprobs_workspace(_logp(vocab=65536), n) == 0 and n.value == 0
+    assert L.mssm_token_logprobs_workspace(_logp(vocab=65537), n) == 0 and n.value == 4 * 19 * 4
+    assert L.mssm_token_logprobs_workspace(_logp(rows=0), n) == DIMS
+    assert L.mssm_token_logprobs_workspace(_logp(), None) == NULL
+    long = _logp(vocab=65537)
+    assert call(long) == WORKSPACE
+    ws, size = BASE - 4096, 4 * 19 * 4 - 1
+    assert call(long) == WORKSPACE
+    ws, size = p["logprobs"], 1 << 20
+    assert call(long) == ALIAS
+    ws = BASE - 4096 + 4
+    assert call(long) == WORKSPACE
 
 
 def test_token_logprobs_backward(L):
@@ -136,8 +154,9 @@ def test_policy_loss(L):
 
     def call(args=None, **o):
         q = {**p, **o}
-        return L.mssm_policy_loss(*[q[n] for n in names], args or _policy(), None)
-    assert L.mssm_policy_loss(*p.values(), None, None) == NULL
+        return L.mssm_policy_loss(*[q[n] for n in names], ws, size, args or _policy(), None)
+    ws, size = None, 0
+    assert L.mssm_policy_loss(*p.values(), None, 0, None, None) == NULL
     for n in ("logits", "tokens", "old", "adv", "loss", "logprobs"):
         assert call(**{n: None}) == NULL, n
     for bad in BAD_LOGP + (dict(gs=10), dict(low=-0.1), dict(high=float("nan")), dict(kl=-1.0),
@@ -148,6 +167,9 @@ def test_policy_loss(L):
     assert call(loss=p["old"]) == ALIAS
     assert call(loss=p["logits"], dlogits=None) == ALIAS
     assert call(logprobs=p["dlogits"] + 8) == ALIAS
+    assert call(_policy(vocab=70000)) == WORKSPACE
+    ws, size = p["dlogits"] + 256, 1 << 20
+    assert call(_policy(vocab=70000)) == ALIAS
 
 
 def test_preference_loss(L):
