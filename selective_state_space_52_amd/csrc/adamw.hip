@@ -20,11 +20,10 @@
 namespace mssm {
 namespace {
 
-// 4 elements a thread in each of 4 passes, so that a wave's accesses are of whole
+// 4 elements a thread in each pass, so that a wave's accesses are of whole
 // neighbouring lines (1 KB of fp32); 32 lanes hold a block.
-constexpr int kThreads = 256, kPer = 4, kUnroll = 4;
-constexpr int kStrip = kThreads * kPer;       // elements of one pass
-constexpr int kElements = kStrip * kUnroll;   // of a workgroup
+constexpr int kThreads = 256, kPer = 4;
+constexpr int kStrip = kThreads * kPer;  // elements of one pass
 constexpr int kBlockLanes = kScaleBlock / kPer;
 constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f;
 constexpr uint32_t kStrideM = 0x9E3779B9u, kStrideV = 0x6A09E667u;
@@ -115,16 +114,16 @@ __device__ __forceinline__ void load4_fp8(float (&v)[4], const void* p, int64_t 
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
 
-// x, of the block that 32 neighbouring lanes hold, as e4m3 at p + i.
-template <bool POSITIVE>
-__device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i, float (&x)[4],
-                                               uint32_t u, uint32_t stride) {
+// x, of the block that 32 neighbouring lanes hold, as e4m3 at p + i.  CAREFUL: with
+// infinities or NaN among them, which become NaN and leave the block's scale
+// alone.  (The vector ALU is what the 8-bit step has least of: 109 instructions an
+// element with these cases everywhere and a fully rounded root, 81 as it is: 209M elements 668 to 645 us.)
+template <bool POSITIVE, bool CAREFUL>
+__device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i,
+                                               const float (&x)[4], uint32_t u, uint32_t stride) {
   float most = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    x[j] = finite_or_nan(x[j]);
-    most = fmaxf(most, fabsf(x[j]));
-  }
+  for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(CAREFUL ? finite_or_nan(x[j]) : x[j]));
   most = max16(most);
   most = fmaxf(most, __shfl_xor(most, 16));
   if (most < kSmallest) most = 0.0f;
@@ -132,15 +131,19 @@ __device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i
   if ((threadIdx.x & (kBlockLanes - 1)) == 0) scales[i / kScaleBlock] = most / kMost8;
   float q[4];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const float y = x[j] * up, a = fabsf(y);
-    // the value's unit: 3 mantissa bits below its power of two, at least 2^-9
-    const uint32_t e = max(__float_as_uint(a) >> 23, 121u);
-    const float unit = __uint_as_float((e - 3) << 23), per = __uint_as_float((257 - e) << 23);
-    const float dither = (float)((u + j * stride) >> 8) * 0x1p-24f;
-    float size = fminf(floorf(__fadd_rn(a * per, dither)) * unit, kMost8);
-    if (POSITIVE && x[j] > 0.0f && most > 0.0f) size = fmaxf(size, 0x1p-9f);
-    q[j] = a == a ? copysignf(size, y) : y;
+  for (int j = 0; j < 4; ++j) {
+    const float y = x[j] * up;
+    // y's power of two, 2^-6 at least; its unit is an eighth of it (3 mantissa bits)
+    const float power = fmaxf(__uint_as_float(__float_as_uint(y) & 0x7F800000u), 0x1p-6f);
+    const float per = __uint_as_float(0x80800000u - __float_as_uint(power));  // 8 / power
+    const float dither = (float)((u + j * stride) >> 8);
+    // |y| per is exact and below 16: one rounding, of the sum
+    float units = floorf(fmaf(dither, 0x1p-24f, fabsf(y) * per));
+    // a root above zero is 2^-75 or more
+    if (POSITIVE) units = fmaxf(units, __builtin_amdgcn_fmed3f(x[j] * 0x1p126f, 0.0f, 1.0f));
+    q[j] = fminf(units * (power * 0.125f), kMost8);
+    if (!POSITIVE) q[j] = copysignf(q[j], y);
+    if (CAREFUL && !(fabsf(x[j]) <= 3.402823466e38f)) q[j] = __builtin_nanf("");
   }
   __builtin_nontemporal_store(pack_fp8x4(q[0], q[1], q[2], q[3]),
                               reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i));
@@ -171,11 +174,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
   t.decay = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.decay), which));
   t.grad_bf16 = __builtin_amdgcn_readlane(mine.grad_bf16, which);
   const uint32_t begins = (uint32_t)__builtin_amdgcn_readlane((int)first, which);
-  const int64_t begin = (int64_t)(blockIdx.x - begins) * kElements;
+  const int64_t begin = (int64_t)(blockIdx.x - begins) * (kStrip * p.passes);
   const Rates r = rates_of(p);
   const float keep = 1.0f - r.lr * t.decay;
-#pragma unroll
-  for (int c = 0; c < kUnroll; ++c) {
+  for (int c = 0; c < p.passes; ++c) {
+#pragma clang fp contract(off)
     const int64_t i = begin + c * kStrip + threadIdx.x * kPer;
     const int64_t left = t.size - i;
     // the states go on to the end of the last block of 128
@@ -207,24 +210,41 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
       load4<false>(m, p.m, at, 4);
       load4<false>(v, p.v, at, 4);
     }
-    float root[4];
+    float root[4], all = 0.0f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       // each product rounded by itself, as the definition reads
-      const float s = __fmul_rn(g[j], r.grad_scale);
-      m[j] = __fadd_rn(__fmul_rn(m[j], p.beta1), __fmul_rn(s, p.rest1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], p.beta2), __fmul_rn(__fmul_rn(s, s), p.rest2));
-      root[j] = sqrtf(v[j]);
-      const float update = m[j] * r.inv_c1 * hw_rcp(root[j] * r.inv_c2 + p.eps);
-      w[j] = w[j] * keep - r.lr * update;
+      const float s = g[j] * r.grad_scale;
+      m[j] = m[j] * p.beta1 + s * p.rest1;
+      v[j] = v[j] * p.beta2 + s * s * p.rest2;
+      float inverse;
+      if constexpr (EIGHT) {
+        // the hardware root (1 unit off), and its residue times half the
+        // reciprocal that the step needs anyway: nearly always the nearest
+        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+        inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
+        const float half = fminf(inverse * (0.5f * r.inv_c2), 3.402823466e38f);
+        root[j] = fmaf(fmaf(-root[j], root[j], v[j]), half, root[j]);
+        all = fmaf(m[j], 0.0f, fmaf(v[j], 0.0f, all));
+      } else {
+        root[j] = sqrtf(v[j]);
+        inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
+      }
+      w[j] = fmaf(-r.lr * r.inv_c1 * m[j], inverse, w[j] * keep);
     }
     if (n > 0) {
       store4<false>(t.param, i, n, w);
       if (t.copy) store4<true>(t.copy, i, n, w);
     }
     if constexpr (EIGHT) {
-      store4_rounded<false>(p.m, p.m_scales, at, m, r.shift_m + (uint32_t)i * kStrideM, kStrideM);
-      store4_rounded<true>(p.v, p.v_scales, at, root, r.shift_v + (uint32_t)i * kStrideV, kStrideV);
+      const uint32_t um = r.shift_m + (uint32_t)i * kStrideM, uv = r.shift_v + (uint32_t)i * kStrideV;
+      if (__ballot(!(all == 0.0f))) {  // infinity or NaN in this wave
+        store4_rounded<false, true>(p.m, p.m_scales, at, m, um, kStrideM);
+        store4_rounded<true, true>(p.v, p.v_scales, at, root, uv, kStrideV);
+      } else {
+        store4_rounded<false, false>(p.m, p.m_scales, at, m, um, kStrideM);
+        store4_rounded<true, false>(p.v, p.v_scales, at, root, uv, kStrideV);
+      }
     } else {
       store4<false>(p.m, at, 4, m);
       store4<false>(p.v, at, 4, v);
@@ -234,7 +254,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
 
 }  // namespace
 
-int64_t adamw_block_elements() { return kElements; }
+// Passes of a workgroup.  fp32 states: one, whose loads wait for nothing (129M
+// elements 676 us; two 696, four 733).  8 bits: four, over which finding the tensor
+// and the rates is spread (209M elements 668 us, one pass 759), but one where
+// there are few (1.2M elements 8.3 us, four passes 12.1; at 9.4M equal).
+int adamw_passes(bool eight, int64_t total) { return eight && total > 8 << 20 ? 4 : 1; }
+int64_t adamw_block_elements(int passes) { return (int64_t)kStrip * passes; }
 
 hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st) {
   auto kernel = eight ? adamw_kernel<true> : adamw_kernel<false>;

@@ -420,6 +420,7 @@ struct LogprobParams {
   int32_t vocab;
   float inv_temperature, clip_lo, clip_hi, kl_coef;
   float* partial;             // workspace: (rows, 2 parts + 1)
+  int32_t odd;                // rows may begin at odd bf16 addresses; set by the launch
   int32_t parts;              // of a long row, 0: whole rows; set by the launch
   int32_t past;               // the gradient is stored past the caches; set by the launch
 };
@@ -466,9 +467,11 @@ struct AdamParams {
   float log_beta1, log_beta2;
   float inv_c1, inv_c2;       // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   int32_t count;
+  int32_t passes;             // of a workgroup
   uint32_t blocks;
 };
-int64_t adamw_block_elements();
+int adamw_passes(bool eight, int64_t total);
+int64_t adamw_block_elements(int passes);
 hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st);
 
 }  // namespace mssm

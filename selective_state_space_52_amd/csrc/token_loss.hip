@@ -15,25 +15,60 @@ namespace {
 
 constexpr float kLowest = -3.402823466e38f;
 
-// 8 columns of a row from i on, -infinity (of probability zero) past its end.
+// A row as the threads see it.  Loads of 16 bytes run at full rate from every
+// multiple of 4 bytes, not from the odd bf16 addresses that every second row of an
+// odd vocabulary begins at (1000 x 200000 80 us, 200003: 108); such a row is taken
+// from the element before it on, which is neither read nor written.
+struct Columns {
+  int64_t from, to;  // of place 0 in the logits and the gradient
+  int skip;          // places before the first column: 0 or 1
+  int end;           // the place behind the last column
+};
 template <bool BF16>
-__device__ __forceinline__ Raw8<BF16> load_columns(const void* p, int64_t from, int i, int vocab) {
+__device__ __forceinline__ Columns columns_of(const LogprobParams& p, int64_t row) {
+  const int64_t from = row * p.logits_stride;
+  const int skip = BF16 && p.odd ? (int)(((uint64_t)p.logits / 2 + (uint64_t)from) & 1) : 0;
+  return Columns{from - skip, row * p.grad_stride - skip, skip, p.vocab + skip};
+}
+
+// 8 places from i on, -infinity (of probability zero) where there is no column.
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> load_columns(const void* p, const Columns& c, int i) {
   Raw8<BF16> r;
-  const int n = vocab - i;
-  if (n >= 8) {
-    r = load_raw8<BF16>(p, from + i);
+  if (i >= c.skip && i + 8 <= c.end) {
+    r = load_raw8<BF16>(p, c.from + i);
   } else if constexpr (BF16) {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + from + i;
-    const auto at = [&](int j) { return j < n ? (uint32_t)q[j] : 0xFF80u; };
+    const uint16_t* q = static_cast<const uint16_t*>(p) + c.from + i;
+    const auto at = [&](int j) {
+      return i + j >= c.skip && i + j < c.end ? (uint32_t)q[j] : 0xFF80u;
+    };
     r.a[0].w[0] = at(0) | at(1) << 16, r.a[0].w[1] = at(2) | at(3) << 16;
-    r.a[0].w[2] = at(4) | at(5) << 16, r.a[0].w[3] = at(6) | 0xFF800000u;
+    r.a[0].w[2] = at(4) | at(5) << 16, r.a[0].w[3] = at(6) | at(7) << 16;
   } else {
-    const uint32_t* q = static_cast<const uint32_t*>(p) + from + i;
-    const auto at = [&](int j) { return j < n ? q[j] : 0xFF800000u; };
+    const uint32_t* q = static_cast<const uint32_t*>(p) + c.from + i;
+    const auto at = [&](int j) { return i + j < c.end ? q[j] : 0xFF800000u; };
     r.a[0].w[0] = at(0), r.a[0].w[1] = at(1), r.a[0].w[2] = at(2), r.a[0].w[3] = at(3);
-    r.a[1].w[0] = at(4), r.a[1].w[1] = at(5), r.a[1].w[2] = at(6), r.a[1].w[3] = 0xFF800000u;
+    r.a[1].w[0] = at(4), r.a[1].w[1] = at(5), r.a[1].w[2] = at(6), r.a[1].w[3] = at(7);
   }
   return r;
+}
+
+// Values at the 8 places from i on.
+template <bool BF16>
+__device__ __forceinline__ void store_columns(const LogprobParams& p, const Columns& c, int i,
+                                              const float (&v)[8]) {
+  if (i < c.skip) {
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      if (i + j >= c.end) break;
+      if constexpr (BF16) static_cast<uint16_t*>(p.dlogits)[c.to + i + j] = to_bf16(v[j]);
+      else static_cast<float*>(p.dlogits)[c.to + i + j] = v[j];
+    }
+  } else if (p.past) {
+    store8_past<BF16>(p.dlogits, c.to + i, c.end - i, v);
+  } else {
+    store8<BF16>(p.dlogits, c.to + i, c.end - i, v);
+  }
 }
 
 template <bool BF16>
@@ -138,16 +173,16 @@ __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, b
   return Row{r.top, log_sum, slope * p.inv_temperature};
 }
 
-// factor * ([i = token] - softmax) of 8 columns from i on.
+// factor * ([column = token] - softmax) at the 8 places from i on.
 template <bool BF16>
-__device__ __forceinline__ void store_slope(const LogprobParams& p, int64_t to, int i, int token,
-                                            const Raw8<BF16>& raw, Row r, float k) {
+__device__ __forceinline__ void store_slope(const LogprobParams& p, const Columns& c, int i,
+                                            int token, const Raw8<BF16>& raw, Row r, float k) {
   float v[8];
   unpack8<BF16>(v, raw);
   const float log_sum2 = r.log_sum * kLog2e;
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = hw_exp2((v[j] - r.top) * k - log_sum2);
-  const uint32_t own = (uint32_t)(token - i);
+  const uint32_t own = (uint32_t)(token + c.skip - i);
   if (own < 8) {  // one thread of a row
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j)
@@ -155,28 +190,21 @@ __device__ __forceinline__ void store_slope(const LogprobParams& p, int64_t to, 
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] *= -r.factor;
-  if (p.past)
-    store8_past<BF16>(p.dlogits, to + i, p.vocab - i, v);
-  else
-    store8<BF16>(p.dlogits, to + i, p.vocab - i, v);
+  store_columns<BF16>(p, c, i, v);
 }
 template <bool BF16>
-__device__ __forceinline__ void store_zeros(const LogprobParams& p, int64_t to, int i, int end,
+__device__ __forceinline__ void store_zeros(const LogprobParams& p, const Columns& c, int i, int end,
                                             int step) {
   const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (; i < end; i += step) {
-    if (p.past)
-      store8_past<BF16>(p.dlogits, to + i, p.vocab - i, zero);
-    else
-      store8<BF16>(p.dlogits, to + i, p.vocab - i, zero);
-  }
+  for (; i < end; i += step) store_columns<BF16>(p, c, i, zero);
 }
 
 // One workgroup of T threads a row that stays in its registers, NV times 8
 // columns a thread: read once.
 template <bool BF16, int T, int NV>
 __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
-  const int64_t row = blockIdx.x, from = row * p.logits_stride, to = row * p.grad_stride;
+  const int64_t row = blockIdx.x;
+  const Columns at = columns_of<BF16>(p, row);
   const int64_t token = p.tokens[row];
   const bool live = token >= 0 && token < p.vocab;
   const float k = p.inv_temperature * kLog2e;
@@ -187,9 +215,9 @@ __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
   if (live) {
 #pragma unroll
     for (int c = 0; c < NV; ++c)
-      raw[c / kEach][c % kEach] = load_columns<BF16>(
-          p.logits, from, min((c * T + (int)threadIdx.x) * 8, p.vocab), p.vocab);
-    taken = logit<BF16>(p.logits, from + token);
+      raw[c / kEach][c % kEach] =
+          load_columns<BF16>(p.logits, at, min((c * T + (int)threadIdx.x) * 8, at.end));
+    taken = logit<BF16>(p.logits, at.from + at.skip + token);
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) take<BF16, kEach>(r, raw[g], k);
     r = of_workgroup<T / 64>(r, k);
@@ -197,7 +225,7 @@ __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
   const Row w = finish_row(p, row, live, r, taken, threadIdx.x == 0);
   if (!p.dlogits) return;
   if (w.factor == 0.0f) {
-    store_zeros<BF16>(p, to, threadIdx.x * 8, p.vocab, T * 8);
+    store_zeros<BF16>(p, at, threadIdx.x * 8, at.end, T * 8);
     return;
   }
   if constexpr (BF16) {
@@ -207,7 +235,7 @@ __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
     const int i = (c * T + threadIdx.x) * 8;
-    if (i < p.vocab) store_slope<BF16>(p, to, i, (int)token, raw[c / kEach][c % kEach], w, k);
+    if (i < at.end) store_slope<BF16>(p, at, i, (int)token, raw[c / kEach][c % kEach], w, k);
   }
 }
 
@@ -215,21 +243,22 @@ __global__ void __launch_bounds__(T) logprob_held_kernel(LogprobParams p) {
 constexpr int kThreads = 1024;
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobParams p) {
-  const int64_t row = blockIdx.x, from = row * p.logits_stride;
+  const int64_t row = blockIdx.x;
+  const Columns at = columns_of<BF16>(p, row);
   const int64_t token = p.tokens[row];
   const bool live = token >= 0 && token < p.vocab;
   const float k = p.inv_temperature * kLog2e;
   Running r{kLowest, 0.0f};
   float taken = 0.0f;
   if (live) {
-    for (int i = threadIdx.x * 8; i < p.vocab; i += kFlight * kThreads * 8) {
+    for (int i = threadIdx.x * 8; i < at.end; i += kFlight * kThreads * 8) {
       Raw8<BF16> raw[kFlight];
 #pragma unroll
       for (int c = 0; c < kFlight; ++c)
-        raw[c] = load_columns<BF16>(p.logits, from, min(i + c * kThreads * 8, p.vocab), p.vocab);
+        raw[c] = load_columns<BF16>(p.logits, at, min(i + c * kThreads * 8, at.end));
       take<BF16, kFlight>(r, raw, k);
     }
-    taken = logit<BF16>(p.logits, from + token);
+    taken = logit<BF16>(p.logits, at.from + at.skip + token);
     r = of_workgroup<kThreads / 64>(r, k);
   }
   finish_row(p, row, live, r, taken, threadIdx.x == 0);
@@ -243,7 +272,8 @@ constexpr int kPartThreads = 256, kColumns = kPartThreads * 8 * kFlight;
 // token's logit too (the gradient may take the logits' place).
 template <bool BF16>
 __global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParams p, int turns) {
-  const int64_t row = blockIdx.x / p.parts, from = row * p.logits_stride;
+  const int64_t row = blockIdx.x / p.parts;
+  const Columns at = columns_of<BF16>(p, row);
   const int part = (int)(blockIdx.x % p.parts);
   const int64_t token = p.tokens[row];
   if (token < 0 || token >= p.vocab) return;
@@ -254,8 +284,8 @@ __global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParam
     Raw8<BF16> raw[kFlight];
 #pragma unroll
     for (int c = 0; c < kFlight; ++c)
-      raw[c] = load_columns<BF16>(
-          p.logits, from, min(first + t * kColumns + c * kPartThreads * 8, p.vocab), p.vocab);
+      raw[c] = load_columns<BF16>(p.logits, at,
+                                  min(first + t * kColumns + c * kPartThreads * 8, at.end));
     take<BF16, kFlight>(r, raw, k);
   }
   r = of_workgroup<kPartThreads / 64>(r, k);
@@ -263,7 +293,7 @@ __global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParam
   float* out = p.partial + row * (2 * p.parts + 1);
   out[2 * part] = r.top;
   out[2 * part + 1] = r.sum;
-  if (part == 0) out[2 * p.parts] = logit<BF16>(p.logits, from + token);
+  if (part == 0) out[2 * p.parts] = logit<BF16>(p.logits, at.from + at.skip + token);
 }
 
 // The row's, by a wave.
@@ -296,8 +326,9 @@ template <bool BF16, bool STATS>
 __global__ void __launch_bounds__(kPartThreads) logprob_bwd_kernel(LogprobParams p, int pieces) {
   const int64_t row = blockIdx.x / pieces;
   const int piece = (int)(blockIdx.x % pieces);
-  const int first = piece * kColumns + threadIdx.x * 8, end = min(p.vocab, (piece + 1) * kColumns);
-  const int64_t token = p.tokens[row], from = row * p.logits_stride, to = row * p.grad_stride;
+  const Columns at = columns_of<BF16>(p, row);
+  const int first = piece * kColumns + threadIdx.x * 8, end = min(at.end, (piece + 1) * kColumns);
+  const int64_t token = p.tokens[row];
   const bool live = token >= 0 && token < p.vocab;
   const float k = p.inv_temperature * kLog2e;
   Row w;
@@ -311,17 +342,17 @@ __global__ void __launch_bounds__(kPartThreads) logprob_bwd_kernel(LogprobParams
                    piece == 0 && threadIdx.x == 0);
   }
   if (w.factor == 0.0f) {
-    store_zeros<BF16>(p, to, first, end, kPartThreads * 8);
+    store_zeros<BF16>(p, at, first, end, kPartThreads * 8);
     return;
   }
   Raw8<BF16> raw[kFlight];
 #pragma unroll
   for (int c = 0; c < kFlight; ++c)
-    raw[c] = load_columns<BF16>(p.logits, from, min(first + c * kPartThreads * 8, p.vocab), p.vocab);
+    raw[c] = load_columns<BF16>(p.logits, at, min(first + c * kPartThreads * 8, at.end));
 #pragma unroll
   for (int c = 0; c < kFlight; ++c) {
     const int i = first + c * kPartThreads * 8;
-    if (i < end) store_slope<BF16>(p, to, i, (int)token, raw[c], w, k);
+    if (i < end) store_slope<BF16>(p, at, i, (int)token, raw[c], w, k);
   }
 }
 
@@ -375,7 +406,7 @@ static int turns_of(int64_t rows, int64_t vocab) {
 }
 static int parts_of(int64_t rows, int64_t vocab) {
   const int64_t each = (int64_t)turns_of(rows, vocab) * kColumns;
-  return vocab <= kHeld ? 0 : (int)((vocab + each - 1) / each);
+  return vocab <= kHeld ? 0 : (int)((vocab + 1 + each - 1) / each);  // one place more: odd rows
 }
 int64_t logprob_workspace(int64_t rows, int64_t vocab) {
   const int64_t parts = parts_of(rows, vocab);
@@ -394,7 +425,7 @@ static hipError_t launch_row(const LogprobParams& p, hipStream_t st) {
                        dim3(kPartThreads), 0, st, p, turns_of(p.rows, p.vocab));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int pieces = (p.vocab + kColumns - 1) / kColumns;
+    const int pieces = (p.vocab + p.odd + kColumns - 1) / kColumns;
     if (p.dlogits)
       hipLaunchKernelGGL((logprob_bwd_kernel<BF16, false>), dim3((unsigned)(p.rows * pieces)),
                          dim3(kPartThreads), 0, st, p, pieces);
@@ -403,12 +434,13 @@ static hipError_t launch_row(const LogprobParams& p, hipStream_t st) {
                          dim3(kPartThreads), 0, st, p);
     return hipGetLastError();
   }
-  if (p.vocab <= 256 * 8) return go(logprob_held_kernel<BF16, 256, 1>, 256);
-  if (p.vocab <= 256 * 8 * 2) return go(logprob_held_kernel<BF16, 256, 2>, 256);
-  if (p.vocab <= 256 * 8 * 4) return go(logprob_held_kernel<BF16, 256, 4>, 256);
-  if (p.vocab <= 1024 * 8 * 2) return go(logprob_held_kernel<BF16, 1024, 2>, 1024);
+  const int places = p.vocab + p.odd;
+  if (places <= 256 * 8) return go(logprob_held_kernel<BF16, 256, 1>, 256);
+  if (places <= 256 * 8 * 2) return go(logprob_held_kernel<BF16, 256, 2>, 256);
+  if (places <= 256 * 8 * 4) return go(logprob_held_kernel<BF16, 256, 4>, 256);
+  if (places <= 1024 * 8 * 2) return go(logprob_held_kernel<BF16, 1024, 2>, 1024);
   if (!p.dlogits) return go(logprob_kernel<BF16>, kThreads);
-  if (p.vocab <= 1024 * 8 * 4) return go(logprob_held_kernel<BF16, 1024, 4>, 1024);
+  if (places <= 1024 * 8 * 4) return go(logprob_held_kernel<BF16, 1024, 4>, 1024);
   return go(logprob_held_kernel<BF16, 1024, 8>, 1024);
 }
 
@@ -418,7 +450,14 @@ static bool goes_past(const LogprobParams& p, bool bf16) {
   return p.rows * p.vocab * (bf16 ? 2 : 4) > (int64_t)64 << 20;
 }
 
+// Whether rows may begin at odd bf16 addresses.  (Where one place more is more than
+// a workgroup holds, they are taken as they lie.)
+static int odd_rows(const LogprobParams& p, bool bf16) {
+  return bf16 && (((uint64_t)p.logits / 2 | (uint64_t)p.logits_stride) & 1) && p.vocab != kHeld;
+}
+
 hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st) {
+  p.odd = odd_rows(p, bf16);
   p.past = goes_past(p, bf16);
   p.parts = parts_of(p.rows, p.vocab);
   return bf16 ? launch_row<true>(p, st) : launch_row<false>(p, st);
@@ -426,7 +465,8 @@ hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st) {
 
 hipError_t launch_logprobs_bwd(LogprobParams p, bool bf16, hipStream_t st) {
   p.past = goes_past(p, bf16);
-  const int pieces = (p.vocab + kColumns - 1) / kColumns;
+  p.odd = odd_rows(p, bf16);
+  const int pieces = (p.vocab + p.odd + kColumns - 1) / kColumns;
   auto kernel = bf16 ? logprob_bwd_kernel<true, true> : logprob_bwd_kernel<false, true>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)(p.rows * pieces)), dim3(kPartThreads), 0, st, p, pieces);
   return hipGetLastError();

@@ -39,8 +39,8 @@ int check_logprob_dims(const mssm_logprob_dims* d, bool grad) {
   if (grad && d->grad_stride != 0 &&
       (d->grad_stride < d->vocab || !fits(d->rows, d->grad_stride)))
     return MSSM_ERR_DIMS;
-  // workgroups of 256 threads take 8192 columns
-  if (!fits(d->rows, (d->vocab + 8191) / 8192, kItems / 256)) return MSSM_ERR_DIMS;
+  // workgroups of 256 threads take 8192 columns, one column more of odd rows
+  if (!fits(d->rows, (d->vocab + 8192) / 8192, kItems / 256)) return MSSM_ERR_DIMS;
   if (!(d->temperature > 0.0f) || !std::isfinite(1.0f / d->temperature) ||
       1.0f / d->temperature == 0.0f)
     return MSSM_ERR_DIMS;
@@ -316,7 +316,8 @@ int mssm_adamw(const mssm_adamw_tensor* tensors, int64_t count, void* m, void* v
     p.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(args->beta2, (double)args->step)));
   }
   // a launch takes tensors up to its table's length and its grid's threads
-  const int64_t per = mssm::adamw_block_elements(), most = kItems / 256;
+  p.passes = mssm::adamw_passes(eight, total);
+  const int64_t per = mssm::adamw_block_elements(p.passes), most = kItems / 256;
   int64_t at = 0, next = 0;
   while (next < count) {
     int64_t blocks = 0;

@@ -9,7 +9,8 @@ from tests import train_common as tc
 pytestmark = pytest.mark.gpu
 U32 = lc.U32
 SHAPES = [(1, 1), (3, 2), (3, 7), (2, 8), (5, 9), (4, 511), (3, 8192), (2, 8193), (2, 16385), (3, 50257),
-          (2, 65536), (1, 70001), (2, 131073), (1, 300007)]
+          (2, 65536), (1, 65537), (1, 70001), (2, 131073),
+          (1, 300007), (5, 65535), (3, 73727)]
 
 
 def inputs(rows, vocab, io, seed=0, pad=0, skip=True):
@@ -167,29 +168,42 @@ def test_masked_logits(io, vocab):
             assert torch.equal(grad[i].cpu(), got[i])
 
 
-def test_strided_rows():
+@pytest.mark.parametrize("vocab,pad,first", [(1003, 5, 3), (8197, 11, 4), (40, 24, 1), (65535, 9, 1),
+                                             (65536, 9, 1), (65536, 8, 3), (70001, 7, 2), (81919, 2, 1),
+                                             (81920, 1, 1)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_strided_rows(vocab, pad, first, io):
+    """Views at any column of wider rows, gradients into such views and in place:
+    the values of whole tensors (sums may be taken in another order where rows
+    begin at an odd address), and nothing written beside them."""
     import selective_state_space_52_amd as m
-    for vocab, pad in ((1003, 5), (8197, 11), (40, 24)):
-        wide, tokens, g = inputs(12, vocab, "bf16", seed=4, pad=pad)
-        view, td = wide.cuda()[:, 3:3 + vocab], tokens.cuda()
-        whole = view.contiguous()
-        logp, stats = m.token_logprobs_fwd(view, td)
-        same = m.token_logprobs_fwd(whole, td)
-        live = (tokens >= 0) & (tokens < vocab)
-        assert torch.equal(logp, same[0]) and torch.equal(stats[live], same[1][live])
-        d = torch.randn(12, device="cuda")
-        out = torch.full((12, vocab + 9), 7.0, dtype=torch.bfloat16, device="cuda")
-        got = m.token_logprobs_bwd(view, td, stats, d, out=out[:, 2:2 + vocab])
-        assert torch.equal(got, m.token_logprobs_bwd(whole, td, stats, d))
-        assert (out[:, :2] == 7).all() and (out[:, 2 + vocab:] == 7).all()     # nothing beside it
-        out.fill_(7.0)
-        loss = m.policy_loss(view, td, logp - 0.1, d, out=out[:, 2:2 + vocab])
-        same = m.policy_loss(whole, td, logp - 0.1, d)
-        assert all(torch.equal(a, b) for a, b in zip(loss, same))
-        assert (out[:, :2] == 7).all() and (out[:, 2 + vocab:] == 7).all()
-        # a view in place
-        again = m.token_logprobs_bwd(view, td, stats, d, out=view)
-        assert torch.equal(again, m.token_logprobs_bwd(whole, td, stats, d))
+    first = min(first, pad)
+    wide, tokens, g = inputs(6, vocab, io, seed=4, pad=pad)
+    wd, td = wide.cuda(), tokens.cuda()
+    view = wd[:, first:first + vocab]
+    plain = view.cpu().contiguous()
+    logp, stats = m.token_logprobs_fwd(view, td)
+    want, top, log_sum, p = tc.logprobs(plain, tokens, 1.0)
+    slack, of_sum, of_p = tc.logprob_slack(plain, tokens, 1.0)
+    live = (tokens >= 0) & (tokens < vocab)
+    lc.bound(logp[live], want[live], slack[live], torch.float32)
+    assert torch.equal(stats[:, 0].cpu()[live], top[live].float())
+    d = torch.randn(6, generator=g)
+    factor = torch.where(live, d.double(), 0.0)
+    out = torch.full((6, vocab + 9), 7.0, dtype=lc.IO[io], device="cuda")
+    got = m.token_logprobs_bwd(view, td, stats, d.cuda(), out=out[:, 2:2 + vocab])
+    check_slope(got, p, tokens, factor, of_p, lc.IO[io])
+    assert (out[:, :2] == 7).all() and (out[:, 2 + vocab:] == 7).all()     # nothing beside it
+    out.fill_(7.0)
+    # slope -adv = d where the ratio is 1
+    again = m.policy_loss(view, td, logp, -d.cuda(), out=out[:, 2:2 + vocab])
+    assert torch.equal(again[1], logp) and torch.equal(again[2], got)
+    assert (out[:, :2] == 7).all() and (out[:, 2 + vocab:] == 7).all()
+    keep = wd.clone()
+    place = m.policy_loss(view, td, logp, -d.cuda(), out=view)
+    assert torch.equal(place[2], got)
+    keep[:, first:first + vocab] = got
+    assert torch.equal(wd, keep)
 
 
 def test_policy_gradient_against_differences():
