@@ -1,7 +1,8 @@
 """A small Mamba-2 language model with 8-bit projections and random weights: a
 prompt through the convolution and the scan, then single tokens through the
-step, the next token sampled on the GPU; and the training step of a layer's norm
-and input projection.
+step, the next token sampled on the GPU; the training step of a layer's norm and
+input projection; and training steps of a small policy from rewards and from
+preferences, its table shared by the embedding and the output projection.
 
 Run: python examples/mamba2_generate.py
 """
@@ -73,7 +74,7 @@ class Model:
     def prompt(self, tokens):
         """tokens (batch, L), L >= 3.  Returns the last tokens' logits and the states."""
         batch, L = tokens.shape
-        x = self.embedding[tokens.flatten()]
+        x = mssm.embedding_fwd(tokens.flatten(), self.embedding)
         residual = torch.zeros(batch * L, self.dim, device=x.device)
         states = []
         for layer in self.layers:
@@ -95,7 +96,7 @@ class Model:
     def step(self, tokens, states, slots=None):
         """tokens (batch,): one more of each sequence; the states are updated in
         place (rows `slots` of them, where given).  Returns the logits."""
-        x = self.embedding[tokens]
+        x = mssm.embedding_fwd(tokens.contiguous(), self.embedding)
         residual = torch.zeros(len(tokens), self.dim, device=x.device)
         for layer, (state, window) in zip(self.layers, states):
             z, xbc, dt, residual = self._project(layer, x, residual)
@@ -143,10 +144,90 @@ class NormLinear(torch.autograd.Function):
         return dx, dresidual, dnorm, dw
 
 
+class Policy:
+    """Logits of the next token from the last one: a table of `vocab` rows, a norm,
+    and the table again.  Parameters fp32 with a bf16 copy of the table for the
+    lookup; the products in 8 bits; AdamW's states in `bits` bits."""
+
+    def __init__(self, dim=128, vocab=500, bits=8, seed=0, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.vocab = vocab
+        self.table = torch.randn(vocab, dim, generator=g, device=device) * 0.05
+        self.norm = torch.ones(dim, device=device)
+        self.params = [self.table, self.norm]
+        self.copies = [self.table.bfloat16(), None]
+        self.moments = mssm.adamw_state(self.params, bits)
+        # on the device, so that a captured step finds them new in every replay
+        self.step = torch.zeros(1, dtype=torch.int64, device=device)
+        self.lr = torch.full((1,), 1e-3, device=device)
+
+    def logits(self, tokens):
+        """Of tokens (rows,), and what the backward needs."""
+        x = mssm.embedding_fwd(tokens, self.copies[0])
+        y, _, rstd = mssm.rms_norm_fwd(x, self.norm, want_rstd=True)
+        out = mssm.fp8_matmul(*mssm.quantize_fp8(y), *mssm.quantize_fp8(self.table, block_rows=128),
+                              out_dtype=torch.float32)
+        return out, (tokens, x, y, rstd)
+
+    def gradients(self, saved, dlogits):
+        """Of the table and the norm, for the logits' gradient."""
+        tokens, x, y, rstd = saved
+        dy = mssm.fp8_matmul(*mssm.quantize_fp8(dlogits),
+                             *mssm.quantize_fp8(self.table, block_rows=128, transpose=True))
+        dtable = mssm.fp8_matmul(*mssm.quantize_fp8(dlogits, transpose=True),
+                                 *mssm.quantize_fp8(y, transpose=True), out_dtype=torch.float32)
+        dx, _, dnorm = mssm.rms_norm_bwd(dy, x, self.norm, rstd)
+        mssm.embedding_bwd(tokens, dx, self.vocab, add_to=dtable)
+        return [dtable, dnorm]
+
+    def update(self, grads):
+        m, v, m_scales, v_scales = self.moments
+        self.step += 1
+        mssm.adamw_step(self.params, grads, m, v, step=self.step, lr=self.lr,
+                        weight_decay=[0.1, 0.0], m_scales=m_scales, v_scales=v_scales,
+                        copies=self.copies)
+
+    def answer(self, tokens, noise):
+        """Sampled next tokens, and their log-probabilities."""
+        logits, _ = self.logits(tokens)
+        taken, _ = mssm.sample_tokens(logits, noise)
+        return taken, mssm.token_logprobs_fwd(logits, taken)[0]
+
+    def reward_step(self, tokens, taken, old_logprobs, advantages, ref_logprobs, weights):
+        """One step on the clipped policy loss; taken is -1 in a prompt's rows.
+        Returns each row's loss and the gradients."""
+        logits, saved = self.logits(tokens)
+        loss, _, dlogits = mssm.policy_loss(logits, taken, old_logprobs, advantages,
+                                            ref_logprobs=ref_logprobs, weights=weights,
+                                            kl_coef=0.05, out=logits)
+        grads = self.gradients(saved, dlogits)
+        self.update(grads)
+        return loss, grads
+
+    def preference_step(self, tokens, taken, ref_logprobs, offsets):
+        """One step on the preference loss of packed pairs.  Returns each pair's
+        loss and the gradients."""
+        logits, saved = self.logits(tokens)
+        logprobs, stats = mssm.token_logprobs_fwd(logits, taken)
+        loss, dlogprobs = mssm.preference_loss(logprobs, ref_logprobs, offsets)
+        dlogits = mssm.token_logprobs_bwd(logits, taken, stats, dlogprobs, out=logits)
+        grads = self.gradients(saved, dlogits)
+        self.update(grads)
+        return loss, grads
+
+
 def main():
     model = Model()
     prompt = torch.randint(0, model.vocab, (4, 32), device="cuda")
     print(model.generate(prompt, 16, temperature=0.8, top_k=50, top_p=0.95))
+    policy = Policy()
+    tokens = torch.randint(0, policy.vocab, (64,), device="cuda")
+    taken, old = policy.answer(tokens, torch.rand(64, policy.vocab, device="cuda"))
+    advantages = (taken % 2).float() * 2 - 1
+    for _ in range(3):
+        loss, _ = policy.reward_step(tokens, taken, old, advantages, old,
+                                     torch.full_like(old, 1 / 64))
+        print(loss.mean().item())
 
 
 if __name__ == "__main__":

@@ -777,7 +777,7 @@ typedef struct {
   float* param;        /* updated in place                                   */
   const void* grad;
   void* copy;          /* bf16, receives the new param; or NULL              */
-  int64_t size;        /* elements, 1 to 2^35                                */
+  int64_t size;        /* elements, 1 to 2^33                                */
   float weight_decay;
   int32_t grad_dtype;  /* mssm_dtype                                         */
 } mssm_adamw_tensor;

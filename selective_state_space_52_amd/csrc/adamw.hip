@@ -20,10 +20,13 @@
 namespace mssm {
 namespace {
 
-// 4 elements a thread in each pass, so that a wave's accesses are of whole
-// neighbouring lines (1 KB of fp32); 32 lanes hold a block.
+// 4 elements a thread, so that a wave's accesses are of whole neighbouring lines
+// (1 KB of fp32); 32 lanes hold a block.  A workgroup of more passes spreads the
+// finding of its tensor over more elements, but its loads wait for the last pass's
+// stores: four passes with fp32 states 734 us for 129M elements, one 676; with
+// 8-bit states 645 and 641 for 209M.
 constexpr int kThreads = 256, kPer = 4;
-constexpr int kStrip = kThreads * kPer;  // elements of one pass
+constexpr int kElements = kThreads * kPer;  // of a workgroup
 constexpr int kBlockLanes = kScaleBlock / kPer;
 constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f;
 constexpr uint32_t kStrideM = 0x9E3779B9u, kStrideV = 0x6A09E667u;
@@ -157,6 +160,7 @@ __device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
 
 template <bool EIGHT>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
+#pragma clang fp contract(off)
   // the tensor whose workgroup this is: the last that begins at or before it.
   // Lane i holds the table's entry i, so that finding the tensor and reading its
   // entry is one wait.
@@ -174,92 +178,90 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
   t.decay = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.decay), which));
   t.grad_bf16 = __builtin_amdgcn_readlane(mine.grad_bf16, which);
   const uint32_t begins = (uint32_t)__builtin_amdgcn_readlane((int)first, which);
-  const int64_t begin = (int64_t)(blockIdx.x - begins) * (kStrip * p.passes);
+  const int64_t begin = (int64_t)(blockIdx.x - begins) * kElements;
   const Rates r = rates_of(p);
   const float keep = 1.0f - r.lr * t.decay;
-  for (int c = 0; c < p.passes; ++c) {
-#pragma clang fp contract(off)
-    const int64_t i = begin + c * kStrip + threadIdx.x * kPer;
-    const int64_t left = t.size - i;
-    // the states go on to the end of the last block of 128
-    if (begin + c * kStrip + (int64_t)(threadIdx.x & ~(kBlockLanes - 1)) * kPer >= t.size) continue;
-    const int n = (int)min((int64_t)kPer, left);
-    float w[4], g[4], m[4], v[4];
-    if (n > 0) {
-      load4<false>(w, t.param, i, n);
-      if (t.grad_bf16)
-        load4<true>(g, t.grad, i, n);
-      else
-        load4<false>(g, t.grad, i, n);
-    } else {
+  const int64_t i = begin + threadIdx.x * kPer;
+  const int64_t left = t.size - i;
+  // the states go on to the end of the last block of 128
+  if (begin + (int64_t)(threadIdx.x & ~(kBlockLanes - 1)) * kPer >= t.size) return;
+  const int n = (int)min((int64_t)kPer, left);
+  float w[4], g[4], m[4], v[4];
+  if (n > 0) {
+    load4<false>(w, t.param, i, n);
+    if (t.grad_bf16)
+      load4<true>(g, t.grad, i, n);
+    else
+      load4<false>(g, t.grad, i, n);
+  } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) w[j] = g[j] = 0.0f;
-    }
-    const int64_t at = t.at + i;
-    if constexpr (EIGHT) {
-      load4_fp8(m, p.m, at);
-      load4_fp8(v, p.v, at);
-      const float ms = p.m_scales[at / kScaleBlock], vs = p.v_scales[at / kScaleBlock];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        m[j] *= ms;
-        v[j] *= vs;
-        v[j] *= v[j];
-      }
-    } else {
-      load4<false>(m, p.m, at, 4);
-      load4<false>(v, p.v, at, 4);
-    }
-    float root[4], all = 0.0f;
+    for (int j = 0; j < kPer; ++j) w[j] = g[j] = 0.0f;
+  }
+  const int64_t at = t.at + i;
+  if constexpr (EIGHT) {
+    load4_fp8(m, p.m, at);
+    load4_fp8(v, p.v, at);
+    const float ms = p.m_scales[at / kScaleBlock], vs = p.v_scales[at / kScaleBlock];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      // each product rounded by itself, as the definition reads
-      const float s = g[j] * r.grad_scale;
-      m[j] = m[j] * p.beta1 + s * p.rest1;
-      v[j] = v[j] * p.beta2 + s * s * p.rest2;
-      float inverse;
-      if constexpr (EIGHT) {
-        // the hardware root (1 unit off), and its residue times half the
-        // reciprocal that the step needs anyway: nearly always the nearest
-        root[j] = __builtin_amdgcn_sqrtf(v[j]);
-        inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
-        const float half = fminf(inverse * (0.5f * r.inv_c2), 3.402823466e38f);
-        root[j] = fmaf(fmaf(-root[j], root[j], v[j]), half, root[j]);
-        all = fmaf(m[j], 0.0f, fmaf(v[j], 0.0f, all));
-      } else {
-        root[j] = sqrtf(v[j]);
-        inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
-      }
-      w[j] = fmaf(-r.lr * r.inv_c1 * m[j], inverse, w[j] * keep);
+      m[j] *= ms;
+      v[j] *= vs;
+      v[j] *= v[j];
     }
-    if (n > 0) {
-      store4<false>(t.param, i, n, w);
-      if (t.copy) store4<true>(t.copy, i, n, w);
-    }
+  } else {
+    load4<false>(m, p.m, at, 4);
+    load4<false>(v, p.v, at, 4);
+  }
+  float root[4], all = 0.0f;
+  uint32_t least = 0xFFFFFFFFu;  // the smallest nonzero v's bits, less one
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    // each product rounded by itself, as the definition reads
+    const float s = g[j] * r.grad_scale;
+    m[j] = m[j] * p.beta1 + s * p.rest1;
+    v[j] = v[j] * p.beta2 + s * s * p.rest2;
+    float inverse;
     if constexpr (EIGHT) {
-      const uint32_t um = r.shift_m + (uint32_t)i * kStrideM, uv = r.shift_v + (uint32_t)i * kStrideV;
-      if (__ballot(!(all == 0.0f))) {  // infinity or NaN in this wave
-        store4_rounded<false, true>(p.m, p.m_scales, at, m, um, kStrideM);
-        store4_rounded<true, true>(p.v, p.v_scales, at, root, uv, kStrideV);
-      } else {
-        store4_rounded<false, false>(p.m, p.m_scales, at, m, um, kStrideM);
-        store4_rounded<true, false>(p.v, p.v_scales, at, root, uv, kStrideV);
-      }
+      // the hardware root (1 unit off), and its residue times half the
+      // reciprocal that the step needs anyway: nearly always the nearest
+      root[j] = __builtin_amdgcn_sqrtf(v[j]);
+      inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
+      const float half = fminf(inverse * (0.5f * r.inv_c2), 3.402823466e38f);
+      root[j] = fmaf(fmaf(-root[j], root[j], v[j]), half, root[j]);
+      all = fmaf(m[j], 0.0f, fmaf(v[j], 0.0f, all));
+      least = min(least, __float_as_uint(v[j]) - 1);
     } else {
-      store4<false>(p.m, at, 4, m);
-      store4<false>(p.v, at, 4, v);
+      root[j] = sqrtf(v[j]);
+      inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
     }
+    w[j] = fmaf(-r.lr * r.inv_c1 * m[j], inverse, w[j] * keep);
+  }
+  if (n > 0) {
+    store4<false>(t.param, i, n, w);
+    if (t.copy) store4<true>(t.copy, i, n, w);
+  }
+  if constexpr (EIGHT) {
+    if (__ballot(least < 0x007FFFFFu)) {  // below 2^-126 the hardware root gives 0
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) root[j] = sqrtf(v[j]);
+    }
+    const uint32_t um = r.shift_m + (uint32_t)i * kStrideM, uv = r.shift_v + (uint32_t)i * kStrideV;
+    if (__ballot(!(all == 0.0f))) {  // infinity or NaN in this wave
+      store4_rounded<false, true>(p.m, p.m_scales, at, m, um, kStrideM);
+      store4_rounded<true, true>(p.v, p.v_scales, at, root, uv, kStrideV);
+    } else {
+      store4_rounded<false, false>(p.m, p.m_scales, at, m, um, kStrideM);
+      store4_rounded<true, false>(p.v, p.v_scales, at, root, uv, kStrideV);
+    }
+  } else {
+    store4<false>(p.m, at, 4, m);
+    store4<false>(p.v, at, 4, v);
   }
 }
 
 }  // namespace
 
-// Passes of a workgroup.  fp32 states: one, whose loads wait for nothing (129M
-// elements 676 us; two 696, four 733).  8 bits: four, over which finding the tensor
-// and the rates is spread (209M elements 668 us, one pass 759), but one where
-// there are few (1.2M elements 8.3 us, four passes 12.1; at 9.4M equal).
-int adamw_passes(bool eight, int64_t total) { return eight && total > 8 << 20 ? 4 : 1; }
-int64_t adamw_block_elements(int passes) { return (int64_t)kStrip * passes; }
+int64_t adamw_block_elements() { return kElements; }
 
 hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st) {
   auto kernel = eight ? adamw_kernel<true> : adamw_kernel<false>;

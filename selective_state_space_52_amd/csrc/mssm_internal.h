@@ -467,11 +467,9 @@ struct AdamParams {
   float log_beta1, log_beta2;
   float inv_c1, inv_c2;       // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   int32_t count;
-  int32_t passes;             // of a workgroup
   uint32_t blocks;
 };
-int adamw_passes(bool eight, int64_t total);
-int64_t adamw_block_elements(int passes);
+int64_t adamw_block_elements();
 hipError_t launch_adamw(const AdamParams& p, bool eight, hipStream_t st);
 
 }  // namespace mssm

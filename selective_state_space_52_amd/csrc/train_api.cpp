@@ -259,8 +259,8 @@ int mssm_adamw(const mssm_adamw_tensor* tensors, int64_t count, void* m, void* v
     const mssm_adamw_tensor& t = tensors[i];
     if (!t.param || !t.grad) return MSSM_ERR_NULL;
     if (!known(t.grad_dtype)) return MSSM_ERR_UNSUPPORTED;
-    // 2^35 elements of one tensor are 2^23 workgroups or fewer
-    if (t.size <= 0 || t.size > (int64_t)1 << 35 || total > (int64_t)1 << 50) return MSSM_ERR_DIMS;
+    // 2^33 elements of one tensor are 2^23 workgroups or fewer
+    if (t.size <= 0 || t.size > (int64_t)1 << 33 || total > (int64_t)1 << 50) return MSSM_ERR_DIMS;
     if (!aligned(t.param, 4) || !aligned(t.grad, size_of(t.grad_dtype)) || !aligned(t.copy, 2))
       return MSSM_ERR_ALIGN;
     total += blocks128(t.size) * 128;
@@ -316,8 +316,7 @@ int mssm_adamw(const mssm_adamw_tensor* tensors, int64_t count, void* m, void* v
     p.inv_c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(args->beta2, (double)args->step)));
   }
   // a launch takes tensors up to its table's length and its grid's threads
-  p.passes = mssm::adamw_passes(eight, total);
-  const int64_t per = mssm::adamw_block_elements(p.passes), most = kItems / 256;
+  const int64_t per = mssm::adamw_block_elements(), most = kItems / 256;
   int64_t at = 0, next = 0;
   while (next < count) {
     int64_t blocks = 0;

@@ -184,6 +184,14 @@ def test_non_finite_and_tiny_gradients():
         mf, vf = m.float(), v.float()
         assert torch.isfinite(mf[ok]).all() and torch.isfinite(vf[ok]).all()
         if bits == 8:
+            # squares below the smallest normal number: their roots are not
+            g = torch.full((128,), 1e-19, device="cuda")
+            q, one = mssm.adamw_state([g], 8), torch.ones(128, device="cuda")
+            mssm.adamw_step([one], [g], q[0], q[1], step=1, lr=0.1, m_scales=q[2], v_scales=q[3])
+            root = q[1].double() * q[3].double()
+            # v is 1e-41, 7000 of the smallest steps: 2^-13 of it, and all are the
+            # block's largest
+            assert float((root / (1e-19 * math.sqrt(1e-3)) - 1).abs().max()) < 2.0 ** -12
             assert torch.isnan(mf[bad]).all() and torch.isnan(vf[bad]).all()
             assert torch.isfinite(ms).all() and torch.isfinite(vs).all()
             assert float(ms[1]) == 0.0 and (mf[128:256] == 0).all() and float(ms[2]) == 0.0
