@@ -232,15 +232,19 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(EmbedBwdParams 
   const int64_t piece = item / q.slices;
   const int lane = threadIdx.x & 63;
   const int col = (int)(item % q.slices) * 512 + lane * 8;
+  const int64_t begin = piece * q.len, last_row = p.rows - 1;
+  // one wait for all of them: places behind the count are in the arrays, and what
+  // they hold is not used
+  const int64_t at = min(begin + lane, last_row);
   const int count = __builtin_amdgcn_readfirstlane(*q.count);
-  const int64_t begin = piece * q.len;
+  const int rows = q.order[at], names = q.named[at];
+  const int prior = q.named[begin > 0 ? min(begin - 1, last_row) : 0];
+  const int next = q.named[min(begin + q.len, last_row)];
   if (begin >= count) return;
   const int len = (int)min((int64_t)q.len, count - begin);
-  const int held = min(lane, len - 1);
-  const int rows = q.order[begin + held], names = q.named[begin + held];
-  bool came_in = begin > 0 && q.named[begin - 1] == __builtin_amdgcn_readfirstlane(names);
+  bool came_in = begin > 0 && prior == __builtin_amdgcn_readfirstlane(names);
   const bool goes_on =
-      begin + len < count && q.named[begin + len] == __builtin_amdgcn_readlane(names, len - 1);
+      begin + len < count && next == __builtin_amdgcn_readlane(names, len - 1);
   const int n = p.dim - col;
   const bool whole = n >= 8;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -337,21 +341,16 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams
     if (wave == 0) load8<false>(sum, q.tail, piece * p.dim + col, n);
     if (ADD && wave == 0) load8<TBF>(old, p.dtable, (int64_t)token * p.dim + col, n);
     const int64_t at = (piece + 1) * p.dim + col;
-    int64_t i = from;
-    for (; i + 8 <= to; i += 8) {
-      float v[8][8];
+    for (int64_t i = from; i < to; i += kRows) {
+      float v[kRows][8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) load8<false>(v[r], q.head, at + (i + r) * p.dim, n);
+      for (int r = 0; r < kRows; ++r) load8<false>(v[r], q.head, at + min(i + r, to - 1) * p.dim, n);
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
+      for (int r = 0; r < kRows; ++r) {
+        if (i + r >= to) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += v[r][j];
-    }
-    for (; i < to; ++i) {
-      float v[8];
-      load8<false>(v, q.head, at + i * p.dim, n);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
     }
   }
 #pragma unroll
