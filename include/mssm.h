@@ -645,7 +645,7 @@ int mssm_mamba2_state_update_workspace(const mssm_step_dims* dims, int64_t* byte
  * fixed order, so equal calls give equal bits.
  */
 typedef struct {
-  int64_t rows;         /* tokens, 1 to 2^31 - 1                              */
+  int64_t rows;         /* tokens, >= 1; rows * ceil(dim / 512) below 2^24    */
   int64_t vocab;        /* rows of the table, 1 to 2^22                       */
   int64_t dim;          /* columns, 1 to 2^20                                 */
   int64_t io_stride;    /* elements from one row of out (dout) to the next;   */
@@ -811,7 +811,7 @@ typedef struct {
  *     its largest value / 448 (0 where that is below 2^-100).  Moments change by
  *     a small part of themselves in a step, which rounding to nearest would
  *     undo; so a value x goes to one of its two e4m3 neighbours at the odds
- *     that keep its mean: to floor(x / unit + u) unit.  u is element i's
+ *     that keep its mean: to floor(x / unit + u) unit (448 at most).  u is element i's
  *     fraction, the upper 24 bits of w + i k (mod 2^32); k = 0x9E3779B9 and w
  *     the lower half of h for m, k = 0x6A09E667 and the upper half for v;
  *     h = y xor (y >> 32) (all mod 2^64) of y = (t xor (t >> 32)) *

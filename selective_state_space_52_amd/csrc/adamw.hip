@@ -1,5 +1,7 @@
 // adamw.hip -- the AdamW step of many tensors in one launch, states in fp32 or
-// in 8 bits.
+// in 8 bits.  Each value is read and written once: HBM bounds both (129M
+// parameters with fp32 states and a bf16 copy 673 us, 209M with 8-bit ones 637: 5.4
+// and 5.3 TB/s), the vector ALU the second nearly so.
 //
 //   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
 //   p = p (1 - lr decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)

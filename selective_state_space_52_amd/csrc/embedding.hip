@@ -4,6 +4,14 @@
 //   dtable[v] = scale * sum of dout[i] over the i with tokens[i] = v  (+ dtable[v])
 //
 // A token outside the table is padding: a zero row, and no gradient.
+//
+// Both move each value once; HBM bounds the large calls, and a call's few waits
+// one after another the small ones.  8192 tokens of a 50304 x 2560 bf16 table 11 us
+// (7.4 TB/s, part of it from the 256 MB cache; its first pass HBM's rate); the
+// gradient of such a table in fp32 121 us: 515 MB are the rows that no token
+// names, cleared beside the sums (8 us the order, 106 sums and clearing at 5.5
+// TB/s, 6 the join).  1777 tokens added to a 50257 x 769 table 20 us, 8 + 9.5 + 4.5
+// in three launches.
 #include <type_traits>
 
 #include "fp8.h"
@@ -49,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(EmbedParams p, int 
 // there.  One launch in place of the several of a digit-by-digit sort; the
 // tokens come from L2.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortRange = 1024;  // most rows of the table a workgroup
+constexpr int kSortRange = 512;  // most rows of the table a workgroup: 32 KB of counts
 
 struct SortPlan {
   int groups, range;
@@ -363,7 +371,9 @@ __global__ void __launch_bounds__(kThreads) embedding_join_kernel(EmbedBwdParams
   finish<TBF, ADD>(p, token, col, sum, old);
 }
 
-// Few rows: one launch and no order.  A workgroup takes a row and 512 columns and
+// Few rows: one launch and no order (81 rows into 28638 x 270: 8 us a call, 24 with
+// the three launches; the comparisons grow with the square of the rows).  A
+// workgroup takes a row and 512 columns and
 // compares the row's token with all others; where no earlier row has it, its
 // waves add up the rows that have it (in parts, added in order).
 constexpr int kDirect = 1024;

@@ -109,6 +109,30 @@ def test_tables_past_32_bits():
     assert not got.view(torch.int16).any()
 
 
+@pytest.mark.parametrize("add", [False, True])
+def test_sorted_rows_of_a_long_table(add):
+    """More rows than are compared directly, into a table of more rows than 256
+    workgroups order."""
+    import selective_state_space_52_amd as m
+    rows, vocab, dim = 2500, (1 << 20) + 5, 9
+    g = torch.Generator().manual_seed(4)
+    t = torch.randint(0, vocab, (rows,), generator=g)
+    t[::3] = torch.randint(vocab - 40, vocab, (len(t[::3]),), generator=g)
+    t[0], t[1] = 0, -1
+    dout = torch.randn(rows, dim, generator=g)
+    old = torch.randn(vocab, dim, generator=g)
+    got = m.embedding_bwd(t.cuda(), dout.cuda(), vocab, add_to=old.cuda() if add else None)
+    live = t >= 0
+    want = torch.zeros(vocab, dim, dtype=torch.float64).index_add_(0, t[live], dout[live].double())
+    size = torch.zeros(vocab, dim, dtype=torch.float64).index_add_(0, t[live], dout[live].double().abs())
+    count = torch.bincount(t[live], minlength=vocab)[:, None]
+    slack = lc.U32 * size * (count + 4)
+    if add:
+        want = want + old.double()
+        slack = slack + lc.U32 * want.abs() * (count > 0)
+    lc.bound(got, want, slack, torch.float32)
+
+
 def test_strided_rows_and_other_streams():
     import selective_state_space_52_amd as m
     g = torch.Generator().manual_seed(1)
