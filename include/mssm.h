@@ -737,7 +737,7 @@ typedef struct {
  * whose loss has no slope (clipped, no KL term) or whose weight is 0 a zero
  * gradient.
  *   old_logprobs, advantages : (rows) fp32
- *   ref_logprobs : (rows) fp32, or NULL (no KL term)
+ *   ref_logprobs : (rows) fp32, or NULL (no KL term; nor with a kl_coef of 0)
  *   weights      : (rows) fp32, or NULL (1)
  *   loss, logprobs : (rows) fp32, unweighted
  *   dlogits      : (rows, vocab) io dtype, or NULL (not computed); it may be
@@ -766,7 +766,7 @@ typedef struct {
  *   logprobs, ref_logprobs : (rows) fp32 (0 in both for a prompt's rows)
  *   offsets   : (2 pairs + 1) int32, not falling, within [0, rows]; a sequence
  *               may be empty.  Values outside count as the nearest inside.
- *   weights   : (pairs) fp32, or NULL (1)
+ *   weights   : (pairs) fp32, or NULL (1); 0 gives its rows 0
  *   loss      : (pairs) fp32, unweighted;  dlogprobs : (rows) fp32
  */
 int mssm_preference_loss(const float* logprobs, const float* ref_logprobs, const int32_t* offsets,

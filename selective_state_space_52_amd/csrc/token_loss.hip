@@ -169,7 +169,11 @@ __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, b
         loss += p.kl_coef * (e - x);
         slope -= p.kl_coef * e;
       }
-      if (p.weights) slope *= p.weights[row];
+      if (p.weights) {
+        // a weight of 0 takes the row out, whatever the loss is there
+        const float w = p.weights[row];
+        slope = w == 0.0f ? 0.0f : slope * w;
+      }
     }
   }
   if (writes) {
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(PreferencePara
   if (threadIdx.x == 0)
     p.loss[pair] = (1.0f - p.smoothing) * minus + p.smoothing * plus;
   const float w = p.weights ? p.weights[pair] : 1.0f;
-  const float slope = (p.smoothing - against) * p.beta * w;
+  const float slope = w == 0.0f ? 0.0f : (p.smoothing - against) * p.beta * w;
   for (int64_t i = at[0] + threadIdx.x; i < at[1]; i += kPairThreads) p.dlogprobs[i] = slope;
   for (int64_t i = at[1] + threadIdx.x; i < at[2]; i += kPairThreads) p.dlogprobs[i] = -slope;
   if (pair == 0)

@@ -211,7 +211,8 @@ int mssm_policy_loss(const void* logits, const int64_t* tokens, const float* old
   mssm::LogprobParams p = logprob_params(d);
   p.partial = static_cast<float*>(workspace);
   p.logits = logits; p.tokens = tokens; p.logprobs = logprobs;
-  p.old_logprobs = old_logprobs; p.advantages = advantages; p.ref_logprobs = ref_logprobs;
+  p.old_logprobs = old_logprobs; p.advantages = advantages;
+  p.ref_logprobs = args->kl_coef > 0.0f ? ref_logprobs : nullptr;  // else no KL term: 0 * inf
   p.weights = weights; p.loss = loss; p.dlogits = dlogits;
   p.clip_lo = 1.0f - args->clip_low; p.clip_hi = 1.0f + args->clip_high;
   p.kl_coef = args->kl_coef;

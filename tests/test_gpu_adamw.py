@@ -229,6 +229,28 @@ def test_device_values_in_a_graph(bits):
         assert (off <= U32 * (a[0].cpu().double().abs() * 2 * k + 8 * 10 * LR * k)).all()
 
 
+def test_a_tensor_past_32_bits():
+    """More than 2^31 elements behind a small tensor: the last ones are stepped, and
+    by fractions of their own."""
+    import selective_state_space_52_amd as mssm
+    n = (1 << 31) + 4000
+    small = torch.ones(5, device="cuda")
+    p = torch.ones(n, device="cuda")
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[-1], g[-200] = -0.25, 0.125
+    m, v, ms, vs = mssm.adamw_state([small, p], 8)
+    mssm.adamw_step([small, p], [torch.ones(5, device="cuda"), g], m, v, step=1, lr=0.1, m_scales=ms,
+                    v_scales=vs, weight_decay=0.0, seed=5)
+    # the first step moves by lr against the gradient's sign, whatever its size
+    for at, sign in ((0, 1), (1 << 31, 1), (n - 1, -1), (n - 200, 1), (n - 2, 1)):
+        assert abs(float(p[at]) - (1 - 0.1 * sign)) < 1e-6
+    assert abs(float(p[::1 << 20].double().mean()) - 0.9) < 1e-6
+    end = 128 + n
+    got = m[128:][n - 200].double() * ms[(end - 200) // 128].double()
+    assert abs(float(got) / 0.0125 - 1) <= 0.125 and float(ms[-1]) > 0
+    assert (m[end:].float() == 0).all()
+
+
 def test_other_stream_and_repeat():
     import selective_state_space_52_amd as mssm
     flat, params, grads, m, v = inputs(SIZES, seed=6)

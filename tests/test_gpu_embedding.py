@@ -48,7 +48,7 @@ KINDS = ["even", "same", "skewed", "padded", "none"]
 @pytest.mark.parametrize("rows,vocab,dim", [(1, 1, 1), (1, 50, 64), (31, 7, 9), (32, 300, 33), (33, 2, 512),
                                             (64, 1000, 520), (257, 257, 130), (1500, 515, 70),
                                             (2100, 40, 1030), (1030, 5000, 8), (1024, 90, 40),
-                                            (1025, 90, 1040)])
+                                            (1025, 90, 1040), (100, 9001, 3), (1100, 9001, 1)])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("io,grad,add", [("bf16", "f32", False), ("f32", "f32", True),
                                          ("bf16", "bf16", True), ("f32", "bf16", False)])

@@ -206,6 +206,47 @@ def test_strided_rows(vocab, pad, first, io):
     assert torch.equal(wd, keep)
 
 
+def test_rows_taken_out():
+    """A weight of 0 leaves nothing of a row or pair in the gradient, whatever its
+    loss is; a KL term of weight 0 is none."""
+    import selective_state_space_52_amd as m
+    logits, tokens, g = inputs(6, 300, "f32", seed=7, skip=False)
+    ld, td = logits.cuda(), tokens.cuda()
+    logp, _ = m.token_logprobs_fwd(ld, td)
+    adv = torch.randn(6, generator=g).cuda()
+    old, w = logp.clone(), torch.ones(6, device="cuda")
+    base = m.policy_loss(ld, td, old, adv, weights=w)[2]
+    old[1], old[2], w[1], w[2] = float("nan"), float("-inf"), 0.0, -0.0
+    ref = torch.full_like(old, float("-inf"))
+    loss, _, grad = m.policy_loss(ld, td, old, adv, ref_logprobs=ref, weights=w, kl_coef=0.0)
+    assert (grad[1:3] == 0).all() and torch.isnan(loss[1])
+    keep = [0, 3, 4, 5]
+    assert torch.equal(grad[keep], base[keep]) and torch.isfinite(loss[keep]).all()
+    at = torch.tensor([0, 1, 3, 4, 6], dtype=torch.int32, device="cuda")
+    _, d = m.preference_loss(old, logp, at, weights=torch.tensor([0.0, 1.0], device="cuda"))
+    assert (d[:3] == 0).all() and (d[3:] != 0).all() and torch.isfinite(d).all()
+
+
+def test_logits_past_32_bits():
+    """Rows whose elements lie beyond 2^31."""
+    import selective_state_space_52_amd as m
+    rows, vocab = 43000, 50304
+    logits = torch.empty(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    logits[-3:] = torch.randn(3, vocab, device="cuda").bfloat16() * 3
+    tokens = torch.full((rows,), -1, device="cuda")
+    tokens[-3:] = torch.tensor([5, 50303, 0], device="cuda")
+    d = torch.ones(rows, device="cuda")
+    few, t3 = logits[-3:].clone(), tokens[-3:].clone()
+    logp, stats = m.token_logprobs_fwd(logits, tokens)
+    want, want_stats = m.token_logprobs_fwd(few, t3)
+    assert torch.equal(logp[-3:], want) and (logp[:-3] == 0).all()
+    grad = m.token_logprobs_bwd(logits, tokens, stats, d)
+    assert torch.equal(grad[-3:], m.token_logprobs_bwd(few, t3, want_stats, d[:3]))
+    assert not grad[:-3].any()
+    _, _, grad = m.policy_loss(logits, tokens, logp, -d, out=grad)
+    assert torch.equal(grad[-3:], m.policy_loss(few, t3, want, -d[:3])[2]) and not grad[:-3].any()
+
+
 def test_policy_gradient_against_differences():
     """Central differences of the 64-bit loss, away from the clip's corners."""
     import selective_state_space_52_amd as m
