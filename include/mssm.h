@@ -674,7 +674,7 @@ int mssm_embedding_fwd(const int64_t* tokens, const void* table, void* out,
  */
 int mssm_embedding_bwd(const int64_t* tokens, const void* dout, void* dtable, void* workspace,
                        int64_t workspace_bytes, const mssm_embed_dims* dims, void* stream);
-/* 0 (then NULL may be given) for up to 1024 rows. */
+/* 0 (then NULL may be given) for up to 512 rows. */
 int mssm_embedding_bwd_workspace(const mssm_embed_dims* dims, int64_t* bytes);
 
 typedef struct {

@@ -56,7 +56,7 @@ def embedding_fwd(tokens, table, scale=1.0, out_dtype=None):
 
 
 # The most rows whose gradient needs no workspace.
-_UNSORTED = 1024
+_UNSORTED = 512
 
 
 def embedding_bwd(tokens, dout, vocab, scale=1.0, out_dtype=torch.float32, add_to=None):

@@ -15,6 +15,8 @@ def tokens_of(kind, rows, vocab, g):
     if kind == "skewed":      # most rows have a few tokens
         few = torch.randint(0, vocab, (3,), generator=g)
         t = torch.where(torch.rand(rows, generator=g) < 0.8, few[torch.randint(0, 3, (rows,), generator=g)], t)
+    elif kind == "ordered":   # a vocabulary in order of frequency
+        t = (vocab ** torch.rand(rows, generator=g, dtype=torch.float64)).long() - 1
     elif kind == "padded":
         out = torch.tensor([-1, vocab, -(1 << 40), 1 << 40, (1 << 32) + 1, -(1 << 63)])
         t = torch.where(torch.rand(rows, generator=g) < 0.5,
@@ -42,13 +44,14 @@ def test_forward(rows, vocab, dim, table, io, scale):
         assert same.dtype == w.dtype and torch.equal(same.cpu(), tc.embedding(t, w, 1.0).to(w.dtype))
 
 
-KINDS = ["even", "same", "skewed", "padded", "none"]
+KINDS = ["even", "same", "skewed", "ordered", "padded", "none"]
 
 
 @pytest.mark.parametrize("rows,vocab,dim", [(1, 1, 1), (1, 50, 64), (31, 7, 9), (32, 300, 33), (33, 2, 512),
                                             (64, 1000, 520), (257, 257, 130), (1500, 515, 70),
                                             (2100, 40, 1030), (1030, 5000, 8), (1024, 90, 40),
-                                            (1025, 90, 1040), (100, 9001, 3), (1100, 9001, 1)])
+                                            (1025, 90, 1040), (100, 9001, 3), (1100, 9001, 1),
+                                            (512, 90, 40), (513, 90, 600)])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("io,grad,add", [("bf16", "f32", False), ("f32", "f32", True),
                                          ("bf16", "bf16", True), ("f32", "bf16", False)])
@@ -78,7 +81,7 @@ def test_backward(rows, vocab, dim, kind, io, grad, add):
     lc.bound(got, want, slack, lc.IO[grad])
 
 
-@pytest.mark.parametrize("kind", ["even", "same", "skewed"])
+@pytest.mark.parametrize("kind", ["even", "same", "skewed", "ordered"])
 def test_backward_long(kind):
     """Many pieces of the order, tokens across hundreds of them."""
     import selective_state_space_52_amd as m

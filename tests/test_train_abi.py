@@ -59,8 +59,8 @@ def test_embedding_backward(L):
         q = {**p, **o}
         return L.mssm_embedding_bwd(*[q[n] for n in names], size, dims or _embed(), None)
     n = ctypes.c_int64(0)
-    assert L.mssm_embedding_bwd_workspace(_embed(rows=1024), n) == 0 and n.value == 0
-    many = dict(rows=1025)
+    assert L.mssm_embedding_bwd_workspace(_embed(rows=512), n) == 0 and n.value == 0
+    many = dict(rows=513)
     assert L.mssm_embedding_bwd_workspace(_embed(**many), n) == 0 and n.value > 0
     need = n.value
     assert L.mssm_embedding_bwd_workspace(_embed(), None) == NULL
