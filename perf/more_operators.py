@@ -127,11 +127,9 @@ def prepare(case, seed):
     if op in ("embed", "embed_bwd"):
         rows, vocab, dim = case["rows"], case["vocab"], case["dim"]
         # tokens whose frequency falls as rank ** -skew, ranks spread over the table
-        # (running sums on the host: on the GPU their order, and with it a token at
-        # an edge, may change from one process to the next)
-        upto = (1.0 + torch.arange(vocab, dtype=torch.float64)).pow(-case.get("skew", 1.0)).cumsum(0)
-        rank = torch.searchsorted((upto / upto[-1]).cuda(), rand(rows).double(), right=True)
-        s["tokens"] = torch.randperm(vocab, generator=g, device="cuda")[rank.clamp(max=vocab - 1)]
+        weight = (1.0 + torch.arange(vocab, device="cuda")).pow(-case.get("skew", 1.0))
+        rank = torch.multinomial(weight, rows, replacement=True, generator=g)
+        s["tokens"] = torch.randperm(vocab, generator=g, device="cuda")[rank]
         if op == "embed":
             s["table"] = randn(vocab, dim, dtype=DTYPES[case["table"]], scale=0.02)
         else:
