@@ -122,7 +122,8 @@ __device__ __forceinline__ void load4_fp8(float (&v)[4], const void* p, int64_t 
 // x, of the block that 32 neighbouring lanes hold, as e4m3 at p + i.  CAREFUL: with
 // infinities or NaN among them, which become NaN and leave the block's scale
 // alone.  (The vector ALU is what the 8-bit step has least of: 109 instructions an
-// element with these cases everywhere and a fully rounded root, 81 as it is: 209M elements 668 to 645 us.)
+// element with these cases everywhere and the compiler's root, 668 us for 209M
+// elements; 87 and 640 with them, and roots below 2^-48, in the waves that hold any.)
 template <bool POSITIVE, bool CAREFUL>
 __device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i,
                                                const float (&x)[4], uint32_t u, uint32_t stride) {
@@ -158,6 +159,18 @@ __device__ __forceinline__ uint64_t of_lane(uint64_t v, int lane) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
   return (uint64_t)hi << 32 | lo;
+}
+
+// The root of x, rounded to nearest: of the hardware's (a unit off at most) and its
+// two neighbours the one that x's distance from their products picks.  For 0, and from
+// 2^-96 on, below which those distances are not exact.
+constexpr uint32_t kLeastSquare = (127u - 96u) << 23;
+__device__ __forceinline__ float near_root(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float down = __uint_as_float(__float_as_uint(s) - 1);
+  const float up = __uint_as_float(__float_as_uint(s) + 1);
+  const float y = fmaf(-down, s, x) <= 0.0f ? down : s;
+  return fmaf(-up, s, x) > 0.0f ? up : y;
 }
 
 template <bool EIGHT>
@@ -222,31 +235,28 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
     const float s = g[j] * r.grad_scale;
     m[j] = m[j] * p.beta1 + s * p.rest1;
     v[j] = v[j] * p.beta2 + s * s * p.rest2;
-    float inverse;
     if constexpr (EIGHT) {
-      // the hardware root (1 unit off), and its residue times half the
-      // reciprocal that the step needs anyway: nearly always the nearest
-      root[j] = __builtin_amdgcn_sqrtf(v[j]);
-      inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
-      const float half = fminf(inverse * (0.5f * r.inv_c2), 3.402823466e38f);
-      root[j] = fmaf(fmaf(-root[j], root[j], v[j]), half, root[j]);
+      root[j] = near_root(v[j]);
       all = fmaf(m[j], 0.0f, fmaf(v[j], 0.0f, all));
       least = min(least, __float_as_uint(v[j]) - 1);
     } else {
       root[j] = sqrtf(v[j]);
-      inverse = hw_rcp(fmaf(root[j], r.inv_c2, p.eps));
     }
-    w[j] = fmaf(-r.lr * r.inv_c1 * m[j], inverse, w[j] * keep);
   }
+  if constexpr (EIGHT) {
+    if (__ballot(least < kLeastSquare - 1)) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) root[j] = sqrtf(v[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    w[j] = fmaf(-r.lr * r.inv_c1 * m[j], hw_rcp(fmaf(root[j], r.inv_c2, p.eps)), w[j] * keep);
   if (n > 0) {
     store4<false>(t.param, i, n, w);
     if (t.copy) store4<true>(t.copy, i, n, w);
   }
   if constexpr (EIGHT) {
-    if (__ballot(least < 0x007FFFFFu)) {  // below 2^-126 the hardware root gives 0
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) root[j] = sqrtf(v[j]);
-    }
     const uint32_t um = r.shift_m + (uint32_t)i * kStrideM, uv = r.shift_v + (uint32_t)i * kStrideV;
     if (__ballot(!(all == 0.0f))) {  // infinity or NaN in this wave
       store4_rounded<false, true>(p.m, p.m_scales, at, m, um, kStrideM);
