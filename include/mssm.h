@@ -807,16 +807,23 @@ typedef struct {
  * step.
  *   state_bits 32: m, v fp32; m_scales and v_scales NULL
  *   state_bits 8 : m, v e4m3 and an fp32 scale for each 128 of them in m_scales,
- *     v_scales: m = value * scale, sqrt(v) = value * scale.  A block's scale is
- *     its largest value / 448 (0 where that is below 2^-100).  Moments change by
+ *     v_scales: m = value * scale, sqrt(v) = value * scale.  A value x is rounded
+ *     with its block's largest one, most (0 where that is below 2^-100), to
+ *       scale = most * (1 / 448);  y = x * (448 * (1 / most)), 0 where most is 0
+ *       value = floor(|y| / unit + u) unit, 448 at most, with x's sign,
+ *     unit the distance of e4m3 values at y (2^-9 below 2^-6).  Moments change by
  *     a small part of themselves in a step, which rounding to nearest would
- *     undo; so a value x goes to one of its two e4m3 neighbours at the odds
- *     that keep its mean: to floor(x / unit + u) unit (448 at most).  u is element i's
- *     fraction, the upper 24 bits of w + i k (mod 2^32); k = 0x9E3779B9 and w
- *     the lower half of h for m, k = 0x6A09E667 and the upper half for v;
- *     h = y xor (y >> 32) (all mod 2^64) of y = (t xor (t >> 32)) *
- *     0x6A09E667F3BCC909, t = (seed + step) * 0x9E3779B97F4A7C15.  No nonzero
- *     sqrt(v) goes to zero.  The step itself uses the unrounded moments.
+ *     undo; this goes to one of two neighbours at the odds that keep the mean.
+ *     u is element i's fraction, the upper 24 bits of w + i k (mod 2^32): k =
+ *     0x9E3779B9 and w the lower half of h for m, k = 0x6A09E667 and the upper half
+ *     for v; h = y xor (y >> 32) (all mod 2^64) of
+ *     y = (t xor (t >> 32)) * 0x6A09E667F3BCC909, t = (seed + step) * 0x9E3779B97F4A7C15.  No nonzero
+ *     sqrt(v) goes to zero (to 2^-9 instead).  The step itself uses the unrounded
+ *     moments.
+ * The states are these formulas in fp32 to the last bit: every operation (1 / 448
+ * and 1 / most among them) is rounded to nearest by itself, left to right, 1 - beta
+ * once from 64 bits; g^2 (1 - beta2) is (g * g) * (1 - beta2), the old v of 8 bits
+ * (value * scale)^2.
  * NaN and infinities stay in their element (as NaN in 8 bits).
  * The list of tensors is read during the call.  Up to 64 tensors take one launch.
  */

@@ -8,14 +8,20 @@
 //
 // The 8-bit states are e4m3 values of m and sqrt(v), not v: the root halves the
 // range in powers of two, and e4m3 with a block's scale spans 2^18 below the
-// block's largest.  Each block of 128 has an fp32 scale, its largest value /
-// 448, so that a block whose values all fall by a thousandth does so in its
+// block's largest.  Each block of 128 has an fp32 scale, its largest value times
+// 1/448, so that a block whose values all fall by a thousandth does so in its
 // scale.  A value goes to one of its two neighbours by a fraction u that has
 // each value's mean kept (rounding to nearest would never let a moment move by
 // less than half a unit, 3% to 6% of it, in a step).  u walks through the
 // elements as a sequence of equal steps modulo 1 (2^32 / golden ratio, and 2^32
 // times the root of 2's fraction for the second state), shifted by a hash of
 // the seed and the step; for one element it is spread evenly over the steps.
+//
+// A last bit decides there whether a value moves by a whole unit, a 16th to an 8th
+// of itself, which every later step then starts from.  So each fp32 operation from
+// the old states and the gradient to the new states is fixed by the definition and
+// rounded to nearest: nothing is contracted or approximated on that way, and equal
+// inputs give equal states by any route.  (The parameter's step feeds nothing back.)
 #include "fp8.h"
 #include "mssm_internal.h"
 
@@ -30,7 +36,7 @@ namespace {
 constexpr int kThreads = 256, kPer = 4;
 constexpr int kElements = kThreads * kPer;  // of a workgroup
 constexpr int kBlockLanes = kScaleBlock / kPer;
-constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f;
+constexpr float kSmallest = 0x1p-100f, kMost8 = 448.0f, kInvMost8 = 1.0f / 448.0f;
 constexpr uint32_t kStrideM = 0x9E3779B9u, kStrideV = 0x6A09E667u;
 
 // v[0..3] = p[i..i+3], the values past `n` >= 1 of them zero.
@@ -133,8 +139,8 @@ __device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i
   most = max16(most);
   most = fmaxf(most, __shfl_xor(most, 16));
   if (most < kSmallest) most = 0.0f;
-  const float up = most > 0.0f ? kMost8 / most : 0.0f;
-  if ((threadIdx.x & (kBlockLanes - 1)) == 0) scales[i / kScaleBlock] = most / kMost8;
+  const float up = most > 0.0f ? kMost8 * (1.0f / most) : 0.0f;
+  if ((threadIdx.x & (kBlockLanes - 1)) == 0) scales[i / kScaleBlock] = most * kInvMost8;
   float q[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -3,6 +3,8 @@ import pytest
 import torch
 
 from tests import layer_common as lc
+from tests import train_common as tc
+from tests.test_gpu_adamw import offsets
 
 pytestmark = pytest.mark.gpu
 U32 = lc.U32
@@ -32,3 +34,110 @@ def test_squares_below_the_normal_numbers(bits, eps):
     want = 1.0 - 0.1 * gd / (gd.abs() + eps)
     off = 0.1 * (2.0 ** -150 * 1.001 / 1e-41 / 2 + 8 * U32)
     assert float((p.double().cpu() - want).abs().max()) <= off + U32
+
+
+def near_root(x):
+    """The nearest fp32 root (torch's own on the CPU is a unit off at places).  One
+    rounded to 53 bits first is at least 2 * 24 + 2 bits wide: the second rounding
+    changes nothing."""
+    return x.double().sqrt().float()
+
+
+def to_8_bits(x, u, positive):
+    """The definition in fp32, each operation of these tensors rounded once."""
+    x, u = x.view(-1, 128), u.view(-1, 128)
+    one, limit = torch.ones(1), torch.full((1,), 448.0)
+    most = x.abs().amax(1, keepdim=True)
+    most = torch.where(most < 2.0 ** -100, 0.0, most)
+    y = x * torch.where(most > 0, limit * (one / most), 0.0)
+    unit = torch.exp2(torch.frexp(y)[1].sub(1).clamp(min=-6).double() - 3).float()
+    value = torch.minimum(torch.floor(y.abs() / unit + u) * unit, limit)
+    if positive:
+        value = torch.where((value == 0) & (y > 0), 2.0 ** -9, value)
+    return torch.copysign(value, y).to(lc.F8).flatten(), (most * (one / limit)).flatten()
+
+
+class Definition:
+    """The states' definition, one tensor after another."""
+
+    def __init__(self, sizes, bits, b1, b2):
+        self.sizes, self.at, self.bits = sizes, offsets(sizes), bits
+        n = self.at[-1]
+        self.m, self.v = torch.zeros(n), torch.zeros(n)           # v: its root in 8 bits
+        if bits == 8:
+            self.m, self.v = self.m.to(lc.F8), self.v.to(lc.F8)
+            self.m_scales, self.v_scales = torch.zeros(n // 128), torch.zeros(n // 128)
+        self.betas = torch.tensor([b1, b2], dtype=torch.float64)
+
+    def step(self, grads, scale, seed, step):
+        """Returns the moments before they go to 8 bits."""
+        b1, b2 = self.betas.float()
+        r1, r2 = (1.0 - self.betas).float()
+        g = torch.zeros(self.at[-1])
+        um, uv = torch.zeros(self.at[-1]), torch.zeros(self.at[-1])
+        for n, a, b, grad in zip(self.sizes, self.at, self.at[1:], grads):
+            g[a:a + n] = grad.float() * torch.tensor(scale)
+            low, high = tc.dither(b - a, seed, step)
+            um[a:b], uv[a:b] = low.float() * 2.0 ** -24, high.float() * 2.0 ** -24
+        m, v = self.m, self.v
+        if self.bits == 8:
+            m = m.float() * self.m_scales.repeat_interleave(128)
+            v = v.float() * self.v_scales.repeat_interleave(128)
+            v = v * v
+        m = m * b1 + g * r1
+        v = v * b2 + (g * g) * r2
+        if self.bits == 8:
+            self.m, self.m_scales = to_8_bits(m, um, False)
+            self.v, self.v_scales = to_8_bits(near_root(v), uv, True)
+        else:
+            self.m, self.v = m, v
+        return m, v
+
+    def same(self, mv, scales):
+        got = list(mv) + [s for s in scales.values() if s is not None]
+        want = [self.m, self.v] + ([self.m_scales, self.v_scales] if self.bits == 8 else [])
+        return all(torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+
+
+def gradients(kind, sizes, g):
+    out = []
+    for i, n in enumerate(sizes):
+        x = torch.randn(n, generator=g) * torch.exp(torch.randn(n, generator=g))
+        if kind == "rare":            # most elements' moments only fall
+            x *= torch.rand(n, generator=g) < 0.05
+        elif kind == "wide":          # from 2^-100 up, blocks of tiny values among them
+            x *= torch.exp2(-100 * torch.rand(n // 64 + 1, generator=g)).repeat_interleave(64)[:n]
+        out.append(x.bfloat16() if i % 2 else x)
+    return out
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("kind", ["plain", "rare", "wide"])
+@pytest.mark.parametrize("betas", [(0.9, 0.95), (0.9, 0.999)])
+def test_states_over_many_steps(bits, kind, betas):
+    """30 steps in a row leave the states that the definition gives, to the last bit:
+    what differs once would move values by whole units later.  Parameters: each step
+    from the step's own start, 16 roundings of the update (of moments whose terms
+    cancel, of those terms), 3 of the parameter."""
+    import selective_state_space_52_amd as mssm
+    sizes = [1, 127, 129, 4097, 60000, 3]
+    seed, scale, lr, eps = 0xFEDCBA9876543210, 0.7, 1e-2, 1e-8
+    g = torch.Generator().manual_seed(17)
+    p = [torch.randn(n, generator=g).cuda() for n in sizes]
+    mv, scales = states(mssm, p, bits)
+    want = Definition(sizes, bits, *betas)
+    for step in range(1, 31):
+        grads = gradients(kind, sizes, g)
+        old = torch.cat(p).double().cpu()
+        before = want.m.double() * want.m_scales.double().repeat_interleave(128) if bits == 8 else want.m.double()
+        mssm.adamw_step(p, [x.cuda() for x in grads], *mv, step=step, lr=lr, betas=betas, eps=eps,
+                        weight_decay=0.1, grad_scale=scale, seed=seed, **scales)
+        m, v = want.step(grads, scale, seed, step)
+        assert want.same(mv, scales), step
+        here = torch.cat([torch.arange(a, a + n) for n, a in zip(sizes, want.at)])
+        by = torch.sqrt(v.double()[here] / (1 - betas[1] ** step)) + eps
+        terms = before[here].abs() * betas[0] + (1 - betas[0]) * scale * torch.cat(
+            [x.double() for x in grads]).abs()
+        update = m.double()[here] / (1 - betas[0] ** step) / by
+        slack = U32 * (16 * lr * terms / (1 - betas[0] ** step) / by + 3 * old.abs())
+        lc.bound(torch.cat(p), old * (1 - lr * 0.1) - lr * update, slack, torch.float32)
