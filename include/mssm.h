@@ -783,7 +783,8 @@ typedef struct {
 } mssm_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps;  /* betas in [0, 1), eps >= 0                 */
+  double lr, beta1, beta2, eps;  /* betas in [0, 1), eps >= 0 (in (0, 2^-126) */
+                                 /* it counts as 2^-126)                      */
   double grad_scale;             /* gradients are multiplied by it            */
   int64_t step;                  /* 1, 2, ...                                 */
   uint64_t seed;                 /* of the 8-bit states' rounding             */
@@ -824,6 +825,8 @@ typedef struct {
  * and 1 / most among them) is rounded to nearest by itself, left to right, 1 - beta
  * once from 64 bits; g^2 (1 - beta2) is (g * g) * (1 - beta2), the old v of 8 bits
  * (value * scale)^2.
+ * With an eps of 0 an element without any gradient so far is
+ * 0 / 0, NaN.
  * NaN and infinities stay in their element (as NaN in 8 bits).
  * The list of tensors is read during the call.  Up to 64 tensors take one launch.
  */

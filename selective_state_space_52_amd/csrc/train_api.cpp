@@ -307,7 +307,9 @@ int mssm_adamw(const mssm_adamw_tensor* tensors, int64_t count, void* m, void* v
   p.lr_value = args->lr_value; p.grad_scale_value = args->grad_scale_value;
   p.step_value = args->step_value;
   p.seed = args->seed; p.step = args->step;
-  p.lr = (float)args->lr; p.grad_scale = (float)args->grad_scale; p.eps = (float)args->eps;
+  p.lr = (float)args->lr; p.grad_scale = (float)args->grad_scale;
+  // the hardware's reciprocal of less is infinite, and its product with a step of 0 NaN
+  p.eps = args->eps > 0.0 ? std::max((float)args->eps, 0x1p-126f) : 0.0f;
   // 1 - beta from the double: from the rounded float it would be 2e-7 off
   p.beta1 = (float)args->beta1; p.rest1 = (float)(1.0 - args->beta1);
   p.beta2 = (float)args->beta2; p.rest2 = (float)(1.0 - args->beta2);

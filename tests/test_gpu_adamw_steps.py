@@ -36,6 +36,21 @@ def test_squares_below_the_normal_numbers(bits, eps):
     assert float((p.double().cpu() - want).abs().max()) <= off + U32
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-30, 1e-40, 1e-300])
+def test_an_eps_below_the_normal_numbers(bits, eps):
+    """A gradient of 0 moves nothing, however small eps is: 0 / eps is 0."""
+    import selective_state_space_52_amd as mssm
+    p, g = torch.ones(300, device="cuda"), torch.zeros(300, device="cuda")
+    g[7] = 3.0
+    mv, scales = states(mssm, [p], bits)
+    for step in (1, 2):
+        mssm.adamw_step([p], [g], *mv, step=step, lr=0.25, eps=eps, weight_decay=0.0, **scales)
+    assert abs(float(p[7]) - 0.5) <= 0.25 * 2.0 ** -3        # 8 bits round its moments
+    p[7] = 1.0
+    assert (p == 1.0).all()
+
+
 def near_root(x):
     """The nearest fp32 root (torch's own on the CPU is a unit off at places).  One
     rounded to 53 bits first is at least 2 * 24 + 2 bits wide: the second rounding
