@@ -825,7 +825,8 @@ typedef struct {
  * and 1 / most among them) is rounded to nearest by itself, left to right, 1 - beta
  * once from 64 bits; g^2 (1 - beta2) is (g * g) * (1 - beta2), the old v of 8 bits
  * (value * scale)^2.
- * With an eps of 0 an element without any gradient so far is
+ * The parameter's step is within 16 roundings of itself (and of its moment's terms,
+ * where they cancel).  With an eps of 0 an element without any gradient so far is
  * 0 / 0, NaN.
  * NaN and infinities stay in their element (as NaN in 8 bits).
  * The list of tensors is read during the call.  Up to 64 tensors take one launch.
