@@ -241,6 +241,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(AdamParams p) {
     const float s = g[j] * r.grad_scale;
     m[j] = m[j] * p.beta1 + s * p.rest1;
     v[j] = v[j] * p.beta2 + s * s * p.rest2;
+  }
+  if (n < kPer) {  // behind the tensor's end zeros stay zeros, also with a scale of infinity
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j >= n) m[j] = v[j] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
     if constexpr (EIGHT) {
       root[j] = near_root(v[j]);
       all = fmaf(m[j], 0.0f, fmaf(v[j], 0.0f, all));

@@ -51,6 +51,27 @@ def test_an_eps_below_the_normal_numbers(bits, eps):
     assert (p == 1.0).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_what_lies_between_tensors_stays_zero(bits, scale, on_device):
+    """Also where the gradients' scale is not finite (a loss scale that overflowed):
+    0 * infinity is no element's."""
+    import selective_state_space_52_amd as mssm
+    sizes = [1, 126, 127, 128, 130, 1023, 4097]
+    p = [torch.ones(n, device="cuda") for n in sizes]
+    mv, scales = states(mssm, p, bits)
+    value = torch.tensor([scale], device="cuda") if on_device else scale
+    mssm.adamw_step(p, [torch.ones_like(x) for x in p], *mv, step=1, lr=0.1, grad_scale=value, **scales)
+    at = offsets(sizes)
+    for t in mv:
+        t = t.float()
+        for n, a, b in zip(sizes, at, at[1:]):
+            assert (t[a + n:b] == 0).all() and not torch.isfinite(t[a:a + n]).any()
+    assert not any(torch.isfinite(x).any() for x in p)
+    assert all(s is None or (s == 0).all() for s in scales.values())
+
+
 def near_root(x):
     """The nearest fp32 root (torch's own on the CPU is a unit off at places).  One
     rounded to 53 bits first is at least 2 * 24 + 2 bits wide: the second rounding
