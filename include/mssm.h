@@ -761,6 +761,7 @@ typedef struct {
  * (preferred) and 2p + 1 (rejected).  With S(s) = sum over a sequence's rows of
  * logprobs - ref_logprobs (in 64 bits) and d = beta (S(2p) - S(2p + 1)):
  *     loss[p] = -(1 - e) log sigmoid(d) - e log sigmoid(-d),  e = label_smoothing
+ * (a term of weight 0 counts nothing, also where d is infinite), and
  *     dlogprobs = weights[p] d(loss[p])/d(logprobs)
  * Rows of no sequence (before the first, behind the last) get 0.
  *   logprobs, ref_logprobs : (rows) fp32 (0 in both for a prompt's rows)

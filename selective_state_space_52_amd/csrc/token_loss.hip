@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(PreferencePara
   const float e = expf(-fabsf(x)), both = log1pf(e);
   const float minus = fmaxf(-x, 0.0f) + both, plus = fmaxf(x, 0.0f) + both;
   const float against = (x > 0.0f ? e : 1.0f) / (1.0f + e);  // sigmoid(-x)
+  // a side of weight 0 counts nothing, also where it is infinite
   if (threadIdx.x == 0)
-    p.loss[pair] = (1.0f - p.smoothing) * minus + p.smoothing * plus;
+    p.loss[pair] = (p.smoothing < 1.0f ? (1.0f - p.smoothing) * minus : 0.0f) +
+                   (p.smoothing > 0.0f ? p.smoothing * plus : 0.0f);
   const float w = p.weights ? p.weights[pair] : 1.0f;
   const float slope = w == 0.0f ? 0.0f : (p.smoothing - against) * p.beta * w;
   for (int64_t i = at[0] + threadIdx.x; i < at[1]; i += kPairThreads) p.dlogprobs[i] = slope;

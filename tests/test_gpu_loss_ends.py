@@ -1,0 +1,35 @@
+"""The losses where a probability is zero, a ratio or a weight at its type's ends."""
+import pytest
+import torch
+
+from tests import layer_common as lc
+
+pytestmark = pytest.mark.gpu
+U32 = lc.U32
+
+
+@pytest.mark.parametrize("smooth", [0.0, 0.2, 1.0])
+@pytest.mark.parametrize("beta", [0.1, -0.1])
+def test_preference_of_impossible_answers(smooth, beta):
+    """A masked token's log-probability is -infinity, so a pair's difference may be
+    infinite: -log sigmoid(+infinity) is 0, of -infinity infinity, and the slope is
+    that of the limit."""
+    import selective_state_space_52_amd as m
+    inf = float("inf")
+    logp = torch.tensor([-1.0, -inf, -2.0, -1.5, -inf, -0.5, -1.0, -1.0])
+    ref = torch.full((8,), -1.25)
+    at = torch.tensor([0, 1, 3, 4, 4, 5, 6, 7, 8], dtype=torch.int32)
+    d = torch.tensor([inf, -0.25, -inf, 0.0], dtype=torch.float64) * beta
+    loss, grad = m.preference_loss(logp.cuda(), ref.cuda(), at.cuda(), beta=beta, label_smoothing=smooth)
+    softplus = lambda x: torch.clamp(x, min=0.0) + torch.log1p(torch.exp(-x.abs()))  # noqa: E731
+    want = torch.zeros(4, dtype=torch.float64)
+    if smooth < 1:
+        want += (1 - smooth) * softplus(-d)
+    if smooth > 0:
+        want += smooth * softplus(d)
+    # d, beta, the smoothing and its difference from 1, two softplus of 4 roundings
+    lc.bound(loss, want, 16 * U32 * (want.nan_to_num(posinf=0.0) + 1), torch.float32)
+    slope = (smooth - 1 / (1 + torch.exp(d))) * beta
+    sides = torch.stack((slope, -slope), 1).flatten()
+    sizes = (at[1:] - at[:-1]).tolist()
+    lc.bound(grad, torch.cat([s.expand(n) for s, n in zip(sides, sizes)]), 16 * U32 * abs(beta), torch.float32)
