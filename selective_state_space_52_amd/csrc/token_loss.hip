@@ -161,12 +161,13 @@ __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, b
     logp = (taken - r.top) * p.inv_temperature - log_sum;
     if (p.old_logprobs) {
       const float ratio = expf(logp - p.old_logprobs[row]), adv = p.advantages[row];
-      const float open = ratio * adv, held = fminf(fmaxf(ratio, p.clip_lo), p.clip_hi) * adv;
+      const float open = ratio * adv;
+      const float held = fminf(fmaxf(ratio, p.clip_lo), p.clip_hi) * adv;
       loss = -(held < open ? held : open);
       slope = held < open ? 0.0f : -open;
       if (p.ref_logprobs) {
         const float x = p.ref_logprobs[row] - logp, e = expm1f(x);
-        loss += p.kl_coef * (e - x);
+        loss += p.kl_coef * (x < __builtin_inff() ? e - x : x);  // infinite, not inf - inf
         slope -= p.kl_coef * e;
       }
       if (p.weights) {

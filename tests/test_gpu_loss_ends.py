@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from tests import layer_common as lc
+from tests import train_common as tc
 
 pytestmark = pytest.mark.gpu
 U32 = lc.U32
@@ -33,3 +34,26 @@ def test_preference_of_impossible_answers(smooth, beta):
     sides = torch.stack((slope, -slope), 1).flatten()
     sizes = (at[1:] - at[:-1]).tolist()
     lc.bound(grad, torch.cat([s.expand(n) for s, n in zip(sides, sizes)]), 16 * U32 * abs(beta), torch.float32)
+
+
+@pytest.mark.parametrize("vocab", [40, 70003])
+def test_policy_with_a_token_of_probability_zero(vocab):
+    """A ratio of 0, clipped or not; the KL estimate of a token that only the
+    reference would take is infinite, of one that only the policy would take too."""
+    import selective_state_space_52_amd as m
+    inf = float("inf")
+    g = torch.Generator().manual_seed(vocab)
+    logits = torch.randn(5, vocab, generator=g)
+    tokens = torch.full((5,), 7)
+    logits[:3, 7] = -inf
+    old, adv = torch.full((5,), -2.0), torch.tensor([1.5, -2.0, 1.5, 0.5, 0.5])
+    logp = tc.logprobs(logits, tokens, 1.0)[0]
+    old[3:] = logp[3:].float()                        # ratios of 1
+    args = [x.cuda() for x in (logits, tokens, old, adv)]
+    loss, got, grad = m.policy_loss(*args)
+    assert (got[:3] == -inf).all() and (grad[:3] == 0).all()
+    lc.bound(loss[:3], torch.tensor([0.0, 1.6, 0.0]), 4 * U32, torch.float32)    # -A times 0, 0.8
+    ref = torch.tensor([-1.0, -1.0, -inf, -inf, -1.0])
+    loss, _, _ = m.policy_loss(*args, ref_logprobs=ref.cuda(), kl_coef=0.1)
+    assert (loss[:2] == inf).all() and float(loss[3]) == inf and torch.isfinite(loss[4])
+    assert torch.isnan(loss[2])                       # -infinity less -infinity is no number
