@@ -161,7 +161,8 @@ __device__ __forceinline__ Row finish_row(const LogprobParams& p, int64_t row, b
     logp = (taken - r.top) * p.inv_temperature - log_sum;
     if (p.old_logprobs) {
       const float ratio = expf(logp - p.old_logprobs[row]), adv = p.advantages[row];
-      const float open = ratio * adv;
+      // an advantage of 0 is none, however large the ratio
+      const float open = adv == 0.0f && ratio > 1.0f ? 0.0f : ratio * adv;
       const float held = fminf(fmaxf(ratio, p.clip_lo), p.clip_hi) * adv;
       loss = -(held < open ? held : open);
       slope = held < open ? 0.0f : -open;
