@@ -683,7 +683,7 @@ typedef struct {
   int64_t logits_stride;  /* elements from one row to the next; 0 = vocab     */
   int64_t grad_stride;    /* the same of dlogits                              */
   int32_t io_dtype;       /* mssm_dtype of logits and dlogits                 */
-  float temperature;      /* > 0, finite                                      */
+  float temperature;      /* > 0, finite, as is log2(e) / temperature         */
 } mssm_logprob_dims;
 
 /*

@@ -41,7 +41,8 @@ int check_logprob_dims(const mssm_logprob_dims* d, bool grad) {
     return MSSM_ERR_DIMS;
   // workgroups of 256 threads take 8192 columns, one column more of odd rows
   if (!fits(d->rows, (d->vocab + 8192) / 8192, kItems / 256)) return MSSM_ERR_DIMS;
-  if (!(d->temperature > 0.0f) || !std::isfinite(1.0f / d->temperature) ||
+  // the kernels multiply by log2(e) / temperature
+  if (!(d->temperature > 0.0f) || !std::isfinite(1.4426950408889634f * (1.0f / d->temperature)) ||
       1.0f / d->temperature == 0.0f)
     return MSSM_ERR_DIMS;
   return MSSM_OK;

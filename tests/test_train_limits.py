@@ -1,0 +1,20 @@
+"""Limits of the ends of a training step that validation holds, and that the Python
+calls know as numbers of their own; nothing here reaches a GPU."""
+import pytest
+
+from tests.test_layer_abi import DIMS, far
+from tests.test_train_abi import L, _logp, _policy  # noqa: F401
+
+
+@pytest.mark.parametrize("t", [1e-45, 2.9e-39, 3.5e-39, 4.2e-39])
+def test_temperatures_too_small_to_divide_by(L, t):  # noqa: F811
+    """log2(e) / t has to be finite: 0 times it, the largest logit's exponent, would
+    be NaN otherwise.  The smallest t is 4.24e-39."""
+    p = far(("logits", "tokens", "logprobs", "stats", "old", "adv", "loss", "dlogits", "d"))
+    at = p.get
+    assert L.mssm_token_logprobs_fwd(at("logits"), at("tokens"), at("logprobs"), at("stats"), None, 0,
+                                     _logp(t=t), None) == DIMS
+    assert L.mssm_token_logprobs_bwd(at("logits"), at("tokens"), at("stats"), at("d"), at("dlogits"),
+                                     _logp(t=t), None) == DIMS
+    assert L.mssm_policy_loss(at("logits"), at("tokens"), at("old"), at("adv"), None, None, at("loss"),
+                              at("logprobs"), at("dlogits"), None, 0, _policy(t=t), None) == DIMS
