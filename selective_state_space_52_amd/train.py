@@ -212,7 +212,8 @@ def preference_loss(logprobs, ref_logprobs, offsets, weights=None, beta=0.1, lab
 
 
 def adamw_state(params, bits=32):
-    """Zero states for adamw_step of these tensors: (m, v, m_scales, v_scales).
+    """Zero states for adamw_step of these tensors (none of them empty): (m, v,
+    m_scales, v_scales).
 
     Each tensor's states begin at a multiple of 128 elements behind the last
     one's.  bits 32: m and v fp32, no scales (None); 8: float8_e4m3fn values and
@@ -222,6 +223,8 @@ def adamw_state(params, bits=32):
         raise ValueError("bits must be 8 or 32")
     if not params:
         raise ValueError("params is empty")
+    if not all(p.numel() for p in params):
+        raise ValueError("a tensor of params is empty: adamw_step takes none")
     dev = params[0].device
     n = sum(-(-p.numel() // 128) for p in params)
     if bits == 32:
@@ -266,7 +269,7 @@ def adamw_step(params, grads, m, v, step, lr, betas=(0.9, 0.999), eps=1e-8, weig
     """AdamW step of many tensors, in place, in one launch for each 64 of them.
 
     params: fp32 tensors; grads: fp32 or bf16, of the same shapes; all
-    contiguous.  m, v, m_scales, v_scales: as adamw_state gives them, for these
+    contiguous, none empty.  m, v, m_scales, v_scales: as adamw_state gives them, for these
     tensors in this order.  step: 1, 2, ...; weight_decay: a number or one for
     each tensor; copies: None, or bf16 tensors (or None) that receive the new
     params; grad_scale multiplies the gradients (1 / loss scale, a clipping

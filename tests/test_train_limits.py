@@ -30,3 +30,12 @@ def test_limits_that_python_knows(L):  # noqa: F811
                              (train._WHOLE, L.mssm_token_logprobs_workspace, lambda k: _logp(vocab=k))):
         assert call(dims(size), n) == 0 and n.value == 0
         assert call(dims(size + 1), n) == 0 and n.value > 0
+
+
+def test_no_states_for_an_empty_tensor():
+    """adamw_step refuses it, so its states are refused too."""
+    import torch
+    import selective_state_space_52_amd as m
+    for bits in (32, 8):
+        with pytest.raises(ValueError):
+            m.adamw_state([torch.zeros(3), torch.zeros(0, 4)], bits)
