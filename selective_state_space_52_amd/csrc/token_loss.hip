@@ -104,7 +104,9 @@ struct Running {
   float top, sum;
 };
 // Adds kFlight times 8 columns, as every kernel here does, so that a row's sum has
-// the same bits in all of them.
+// the same bits in all of them, and in calls of any number of rows.  (A bf16 row that
+// begins at an odd address is grouped from one column earlier than one that does not:
+// the same row at addresses of both parities may differ in its sum's last bits.)
 constexpr int kFlight = 4;
 template <bool BF16, int N>
 __device__ __forceinline__ void take(Running& r, Raw8<BF16> (&raw)[N], float k) {
@@ -284,10 +286,12 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobParams p) {
 // launch joins and, for the gradient, reads the logits again.
 constexpr int kPartThreads = 256, kColumns = kPartThreads * 8 * kFlight;
 
-// A workgroup sums `turns` times kColumns columns; the first of a row keeps the
-// token's logit too (the gradient may take the logits' place).
+// A workgroup sums kColumns columns, so that a row's sum goes by its length alone and
+// not by how many rows the call has (2 to 8 times as many columns for a workgroup
+// where the rows are many: 1000 x 200003 204 to 212 us, so 202).  The first of a row
+// keeps the token's logit too (the gradient may take the logits' place).
 template <bool BF16>
-__global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParams p, int turns) {
+__global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParams p) {
   const int64_t row = blockIdx.x / p.parts;
   const Columns at = columns_of<BF16>(p, row);
   const int part = (int)(blockIdx.x % p.parts);
@@ -295,15 +299,12 @@ __global__ void __launch_bounds__(kPartThreads) logprob_part_kernel(LogprobParam
   if (token < 0 || token >= p.vocab) return;
   const float k = p.inv_temperature * kLog2e;
   Running r{kLowest, 0.0f};
-  const int first = part * turns * kColumns + threadIdx.x * 8;
-  for (int t = 0; t < turns; ++t) {
-    Raw8<BF16> raw[kFlight];
+  const int first = part * kColumns + threadIdx.x * 8;
+  Raw8<BF16> raw[kFlight];
 #pragma unroll
-    for (int c = 0; c < kFlight; ++c)
-      raw[c] = load_columns<BF16>(p.logits, at,
-                                  min(first + t * kColumns + c * kPartThreads * 8, at.end));
-    take<BF16, kFlight>(r, raw, k);
-  }
+  for (int c = 0; c < kFlight; ++c)
+    raw[c] = load_columns<BF16>(p.logits, at, min(first + c * kPartThreads * 8, at.end));
+  take<BF16, kFlight>(r, raw, k);
   r = of_workgroup<kPartThreads / 64>(r, k);
   if (threadIdx.x != 0) return;
   float* out = p.partial + row * (2 * p.parts + 1);
@@ -417,17 +418,11 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(PreferencePara
 // Columns that a workgroup of 1024 threads can hold.
 constexpr int64_t kHeld = 1024 * 8 * 8;
 
-// Turns of a part: one, or as many (up to 8) as leave 2048 workgroups.
-static int turns_of(int64_t rows, int64_t vocab) {
-  const int64_t turns = rows * ((vocab + kColumns - 1) / kColumns) / 2048;
-  return (int)(turns < 1 ? 1 : turns > 8 ? 8 : turns);
-}
-static int parts_of(int64_t rows, int64_t vocab) {
-  const int64_t each = (int64_t)turns_of(rows, vocab) * kColumns;
-  return vocab <= kHeld ? 0 : (int)((vocab + 1 + each - 1) / each);  // one place more: odd rows
+static int parts_of(int64_t vocab) {
+  return vocab <= kHeld ? 0 : (int)((vocab + 1 + kColumns - 1) / kColumns);  // one place more: odd rows
 }
 int64_t logprob_workspace(int64_t rows, int64_t vocab) {
-  const int64_t parts = parts_of(rows, vocab);
+  const int64_t parts = parts_of(vocab);
   return parts ? rows * (2 * parts + 1) * 4 : 0;
 }
 
@@ -440,7 +435,7 @@ static hipError_t launch_row(const LogprobParams& p, hipStream_t st) {
   };
   if (p.parts) {
     hipLaunchKernelGGL(logprob_part_kernel<BF16>, dim3((unsigned)(p.rows * p.parts)),
-                       dim3(kPartThreads), 0, st, p, turns_of(p.rows, p.vocab));
+                       dim3(kPartThreads), 0, st, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int pieces = (p.vocab + p.odd + kColumns - 1) / kColumns;
@@ -477,7 +472,7 @@ static int odd_rows(const LogprobParams& p, bool bf16) {
 hipError_t launch_logprobs(LogprobParams p, bool bf16, hipStream_t st) {
   p.odd = odd_rows(p, bf16);
   p.past = goes_past(p, bf16);
-  p.parts = parts_of(p.rows, p.vocab);
+  p.parts = parts_of(p.vocab);
   return bf16 ? launch_row<true>(p, st) : launch_row<false>(p, st);
 }
 

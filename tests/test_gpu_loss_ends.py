@@ -74,3 +74,25 @@ def test_policy_with_ratios_past_fp32(vocab):
     assert (loss[:2] == 0).all() and (grad[:3] == 0).all()
     lc.bound(loss[2:3], torch.tensor([-2.4]), 8 * U32, torch.float32)
     assert float(loss[3]) == inf and torch.isnan(loss[4])
+
+
+@pytest.mark.parametrize("vocab,io", [(70002, "bf16"), (131072, "bf16"), (70001, "f32"), (50304, "bf16"),
+                                      (50257, "f32"), (12000, "bf16")])
+def test_rows_alone_and_among_many(vocab, io):
+    """A row's log-probability has the same bits in a call of many rows and in one of a
+    few, so samples that were scored in one call train in smaller ones with ratios of
+    exactly 1; with and without the gradient."""
+    import selective_state_space_52_amd as m
+    rows = 1024
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    logits = torch.randn(rows, vocab, generator=g, device="cuda").to(lc.IO[io])
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    logp, stats = m.token_logprobs_fwd(logits, tokens)
+    adv = torch.ones(rows, device="cuda")
+    for n in (1, 6, 130):
+        for at in (0, rows - n):
+            part = slice(at, at + n)
+            few, few_stats = m.token_logprobs_fwd(logits[part], tokens[part])
+            assert torch.equal(few, logp[part]) and torch.equal(few_stats, stats[part])
+            loss, again, _ = m.policy_loss(logits[part], tokens[part], logp[part], adv[part])
+            assert torch.equal(again, few) and (loss == -1).all()
