@@ -1,7 +1,7 @@
 // adamw.hip -- the AdamW step of many tensors in one launch, states in fp32 or
 // in 8 bits.  Each value is read and written once: HBM bounds both (129M
-// parameters with fp32 states and a bf16 copy 673 us, 209M with 8-bit ones 637: 5.4
-// and 5.3 TB/s), the vector ALU the second nearly so.
+// parameters with fp32 states and a bf16 copy 673 us, 209M with 8-bit ones 630: 5.4
+// TB/s), the vector ALU the second nearly so.
 //
 //   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
 //   p = p (1 - lr decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
@@ -64,7 +64,9 @@ __device__ __forceinline__ void load4(float (&v)[4], const void* p, int64_t i, i
     }
   }
 }
-// Past the caches: a step's data are more than they hold, and not read again soon.
+// Past the caches: a large step's data are more than they hold, and not read again
+// soon.  (Through them 129M parameters 698 us, past them 670; from 6M to 47M the same,
+// also with a read of the copy after the step; below, that read is 1 us slower.)
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 template <bool BF16>
 __device__ __forceinline__ void store4(void* p, int64_t i, int n, const float (&v)[4]) {
@@ -129,7 +131,7 @@ __device__ __forceinline__ void load4_fp8(float (&v)[4], const void* p, int64_t 
 // infinities or NaN among them, which become NaN and leave the block's scale
 // alone.  (The vector ALU is what the 8-bit step has least of: 109 instructions an
 // element with these cases everywhere and the compiler's root, 668 us for 209M
-// elements; 87 and 640 with them, and roots below 2^-48, in the waves that hold any.)
+// elements; 92 and 635 with them, and roots below 2^-48, in the waves that hold any.)
 template <bool POSITIVE, bool CAREFUL>
 __device__ __forceinline__ void store4_rounded(void* p, float* scales, int64_t i,
                                                const float (&x)[4], uint32_t u, uint32_t stride) {

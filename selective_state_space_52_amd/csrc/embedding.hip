@@ -6,12 +6,12 @@
 // A token outside the table is padding: a zero row, and no gradient.
 //
 // Both move each value once; HBM bounds the large calls, and a call's few waits
-// one after another the small ones.  8192 tokens of a 50304 x 2560 bf16 table 11 us
-// (7.4 TB/s, part of it from the 256 MB cache; its first pass HBM's rate); the
-// gradient of such a table in fp32 121 us: 515 MB are the rows that no token
-// names, cleared beside the sums (8 us the order, 106 sums and clearing at 5.5
-// TB/s, 6 the join).  1777 tokens added to a 50257 x 769 table 20 us, 8 + 9.5 + 4.5
-// in three launches.
+// one after another the small ones.  8192 tokens of a 50304 x 2560 bf16 table 11.5 us
+// (a text's spread names 3360 rows: 17 MB read and 42 written, 5.1 TB/s); the
+// gradient of such a table in fp32 124 us: 515 MB are the table's rows, most of them
+// cleared beside the sums (12 us the order, 107 sums and clearing at 5.3 TB/s, 6 the
+// join).  1777 tokens added to a 50257 x 769 table 21 us, 7.5 + 9.6 + 4.5 in three
+// launches.
 #include <type_traits>
 
 #include "fp8.h"
@@ -171,9 +171,10 @@ __global__ void __launch_bounds__(kSortThreads)
         continue;
       }
       // the lanes with this lane's token, from a ballot for each of its bits; the
-      // first of them takes places for all.  (One lane a turn, as above, took 470
-      // us for 65536 tokens half of which fell in one range, as a vocabulary in
-      // order of frequency has it; this alone 12 us for 8192 spread ones, both 8.)
+      // first of them takes places for all.  (One lane a turn, as above, takes 470 us
+      // for 65536 tokens half of which fall in one range, as a vocabulary in order of
+      // frequency has it, and both 68.  This alone 9 and 35 us for 8192 and 65536
+      // evenly spread tokens, both 7.3 and 26; for 8192 of a text 11.5 and 11.6.)
       const uint32_t id = in ? (uint32_t)own : (uint32_t)kSortRange;
       uint64_t same = ~0ull;
 #pragma unroll

@@ -14,7 +14,7 @@
 // that: a row held in registers between its sum and its gradient (read twice: 175
 // us), loads of 4 to 8 times 16 bytes a thread in flight, gradients past the caches
 // (138 us through them).  A row too long for that is read twice, by two launches
-// (1000 x 200003 201 us; the second read costs as much as the first, also when
+// (1000 x 200003 198 us; the second read costs as much as the first, also when
 // the rows are taken in groups that the 256 MB cache holds).  fp32 rows above 32768
 // leave room for one workgroup a CU: 2048 x 50304 200 us, 4.1 TB/s, in parts 243.
 #include "fp8.h"
