@@ -818,8 +818,8 @@ typedef struct {
  *     undo; this goes to one of two neighbours at the odds that keep the mean.
  *     u is element i's fraction, the upper 24 bits of w + i k (mod 2^32): k =
  *     0x9E3779B9 and w the lower half of h for m, k = 0x6A09E667 and the upper half
- *     for v; h = y xor (y >> 32) (all mod 2^64) of
- *     y = (t xor (t >> 32)) * 0x6A09E667F3BCC909, t = (seed + step) * 0x9E3779B97F4A7C15.  No nonzero
+ *     for v; h = z xor (z >> 32) (all mod 2^64) of z = (t xor (t >> 32)) *
+ *     0x6A09E667F3BCC909, t = (seed + step) * 0x9E3779B97F4A7C15.  No nonzero
  *     sqrt(v) goes to zero (to 2^-9 instead).  The step itself uses the unrounded
  *     moments.
  * The states are these formulas in fp32 to the last bit: every operation (1 / 448
